@@ -372,6 +372,145 @@ nvfp4_status_t nvfp4_swizzle_scales(const uint8_t *compact, int64_t rows, int64_
  * (0 for a negative or empty shape, or 2^32 or more rows or scale columns). */
 uint64_t nvfp4_swizzled_scales_bytes(int64_t rows, int64_t scale_cols);
 
+/* ---------------------------------------------------------------------------
+ * Expert layers: tokens sorted by expert and back, block-scaled FP8
+ * operands, and their products. These calls follow the conventions above
+ * (device buffers, host-side checks, no allocation, no synchronization);
+ * index arrays hold int32. Sums are held in FP32 and outputs rounded once
+ * (nearest even). A call gives the same bits every time.
+ * ------------------------------------------------------------------------- */
+
+/* Rows that the tokens of a sort need at most, whatever the ids are:
+ * tokens * topk, plus align - 1 for each expert that can have a token, down
+ * to a multiple of align. 0 for arguments that nvfp4_expert_sort refuses. */
+uint64_t nvfp4_expert_rows(int64_t tokens, int64_t topk, int64_t experts, int64_t align);
+
+/* Bytes of nvfp4_expert_sort's workspace: 0 up to 4096 slots. */
+uint64_t nvfp4_expert_sort_workspace_bytes(int64_t tokens, int64_t topk, int64_t experts);
+
+/*
+ * Sort the slots of a router by expert. ids [tokens][topk] holds int32
+ * (id_bytes 4) or int64 (id_bytes 8) expert numbers; slot s = token * topk + j.
+ * An id outside 0 .. experts - 1 drops its slot. The slots of one expert get
+ * consecutive rows in the order of the slots, each expert's first row being a
+ * multiple of align (a power of two up to 128), experts in order.
+ *   slot_rows [tokens][topk]: the slot's row, -1 if dropped;
+ *   row_slots [rows]: the row's slot, -1 in padding;
+ *   offsets [experts + 1]: each expert's first row; [experts]: the first row
+ *     past them all (with align 16 the differences suit
+ *     nvfp4_quantize_grouped, with 128 its swizzled scales and
+ *     nvfp4_fp8_matmul_grouped_k as well);
+ *   counts [experts]: each expert's slots, padding left out.
+ * experts in 1 .. NVFP4_MAX_GROUPS, tokens * topk < 2^31, rows at least
+ * nvfp4_expert_rows() and < 2^31. workspace: 4-byte aligned, at least
+ * nvfp4_expert_sort_workspace_bytes() (NULL if that is 0); its contents do
+ * not matter. One launch up to 4096 slots, else two.
+ */
+nvfp4_status_t nvfp4_expert_sort(const void *ids, uint32_t id_bytes, int64_t tokens, int64_t topk, int64_t experts,
+                                 int64_t align, int64_t rows, int32_t *slot_rows, int32_t *row_slots,
+                                 int32_t *offsets, int32_t *counts, void *workspace, void *stream);
+
+/*
+ * Tokens to the sorted rows: y[r] = x[row_slots[r] / topk], zeros where
+ * row_slots[r] is not a slot (0 .. tokens * topk - 1). x is [tokens][cols],
+ * y [rows][cols], both of `dtype` and 16-byte aligned; any cols.
+ */
+nvfp4_status_t nvfp4_expert_gather(const void *x, nvfp4_dtype_t dtype, int64_t tokens, int64_t topk, int64_t cols,
+                                   const int32_t *row_slots, int64_t rows, void *y, void *stream);
+
+/*
+ * Sorted rows back to tokens: out[t] = sum over j of weights[t][j] *
+ * y[slot_rows[t][j]], leaving out the slots whose row is not in 0 .. rows - 1;
+ * their rows are not read. weights FP32 [tokens][topk], or NULL for ones:
+ * with the gradient of nvfp4_expert_gather's output as y that gives the
+ * gradient of its input. y [rows][cols], out [tokens][cols], as above.
+ */
+nvfp4_status_t nvfp4_expert_combine(const void *y, nvfp4_dtype_t dtype, int64_t tokens, int64_t topk, int64_t cols,
+                                    const int32_t *slot_rows, int64_t rows, const float *weights, void *out,
+                                    void *stream);
+
+/*
+ * Gradients of nvfp4_expert_combine with weights, from dout [tokens][cols]
+ * and the y that it read: dy[r] = weights[s] * dout[s / topk] with s =
+ * row_slots[r], zeros where that is no slot; dweights[s] (FP32) = the dot
+ * product of dout[s / topk] and y[slot_rows[s]], 0 for a dropped slot.
+ * slot_rows and row_slots come from one sort (each other's inverse).
+ */
+nvfp4_status_t nvfp4_expert_combine_grad(const void *dout, const void *y, nvfp4_dtype_t dtype, int64_t tokens,
+                                         int64_t topk, int64_t cols, const int32_t *slot_rows,
+                                         const int32_t *row_slots, int64_t rows, const float *weights, void *dy,
+                                         float *dweights, void *stream);
+
+/* A block-scaled FP8 matrix of n rows of k values.
+ *   data   OCP E4M3 bytes [n][nvfp4_fp8_pitch(k)]; bytes k .. of a row are
+ *          zero. 16-byte aligned.
+ *   scales FP32 decode scales, block by block along k: [ceil(k / 128)][n]
+ *          for 1x128 blocks, [ceil(k / 128)][ceil(n / 128)] for 128x128
+ *          blocks. 4-byte aligned.
+ * A batch has its matrices one after the other in both arrays. */
+typedef struct {
+  uint8_t *data;
+  float *scales;
+} nvfp4_fp8_t;
+
+/* Bytes of one row: k rounded up to a multiple of 128 (0 for k <= 0). */
+uint64_t nvfp4_fp8_pitch(int64_t k);
+
+/*
+ * Quantize a batch of matrices x [batch][rows][cols] (16-byte aligned, any
+ * sizes) to block-scaled FP8, into the row-wise orientation (n = rows, k =
+ * cols), the column-wise one (the transpose: n = cols, k = rows), or both from
+ * one read; row or col may be NULL, not both. block_2d 0: 1x128 blocks along
+ * each orientation's rows; 1: 128x128 blocks, whose scales both orientations
+ * share (transposed).
+ * Per block: s = fl(max|v| / 448), e = fl(1 / s) (0 when s == 0, at most
+ * FLT_MAX), code = E4M3(fl(v * e)), nearest even, saturating at 448. The
+ * rows and columns that a block lacks count as zeros. A block with a NaN has
+ * a NaN scale, one with an infinity an infinite one.
+ * With row_slots (int32 [rows], batch 1): x is [tokens][cols] and row r of the
+ * matrix is x[row_slots[r] / topk], zeros where row_slots[r] is not a slot
+ * (0 .. tokens * topk - 1): nvfp4_expert_gather and this call in one. Without
+ * it tokens and topk are ignored.
+ */
+nvfp4_status_t nvfp4_fp8_quantize(const void *x, nvfp4_dtype_t dtype, int64_t batch, int64_t rows, int64_t cols,
+                                  const int32_t *row_slots, int64_t tokens, int64_t topk, uint32_t block_2d,
+                                  const nvfp4_fp8_t *row, const nvfp4_fp8_t *col, void *stream);
+
+/*
+ * d = a b^T: a has m rows of k values in 1x128 blocks, b has n rows of k
+ * values in 1x128 blocks or (b_block_2d) 128x128 blocks, d is [m][n] of
+ * d_dtype, 16-byte aligned. Any m, n; k < 2^23; k = 0 gives zeros. With the
+ * orientations of nvfp4_fp8_quantize: y = x w^T takes x row-wise and w
+ * row-wise, dx = dy w takes dy row-wise and w column-wise, dw = dy^T x takes
+ * both column-wise.
+ */
+nvfp4_status_t nvfp4_fp8_matmul(const nvfp4_fp8_t *a, const nvfp4_fp8_t *b, int64_t m, int64_t n, int64_t k,
+                                uint32_t b_block_2d, void *d, nvfp4_dtype_t d_dtype, void *stream);
+
+/*
+ * The experts' products: rows offsets[g] .. offsets[g + 1] - 1 of a (1x128
+ * blocks, `rows` rows) are multiplied by matrix g of the batch b [groups] (n
+ * rows of k values, 128x128 blocks each); rows from offsets[groups] on are set
+ * to zero. offsets: int32 [groups + 1] in device memory, non-decreasing from 0
+ * to at most rows, as nvfp4_expert_sort writes them; contents that are not
+ * leave rows of d unwritten or written twice, but stay inside the buffers.
+ */
+nvfp4_status_t nvfp4_fp8_matmul_grouped(const nvfp4_fp8_t *a, const nvfp4_fp8_t *b, const int32_t *offsets,
+                                        int64_t groups, int64_t rows, int64_t n, int64_t k, void *d,
+                                        nvfp4_dtype_t d_dtype, void *stream);
+
+/*
+ * The experts' weight gradients: for each group g, d[g] [m][n] = the product
+ * a b^T over columns offsets[g] .. offsets[g + 1] - 1 of a (m rows of k values)
+ * and b (n rows of k values), both in 1x128 blocks: with the sorted rows as k,
+ * the column-wise orientations of dy and x. Offsets as above, and multiples
+ * of 128 (a sort with align 128), so that no block belongs to two groups. An
+ * empty group's d is zero. d is [groups][m][n]; k < 2^23.
+ */
+nvfp4_status_t nvfp4_fp8_matmul_grouped_k(const nvfp4_fp8_t *a, const nvfp4_fp8_t *b, const int32_t *offsets,
+                                          int64_t groups, int64_t m, int64_t n, int64_t k, void *d,
+                                          nvfp4_dtype_t d_dtype, void *stream);
+
 /* Text for the last non-OK status returned on the calling thread ("" when
  * none). The pointer stays valid until the next call on that thread. */
 const char *nvfp4_last_error(void);

@@ -14,6 +14,7 @@ Tensors passed in are torch CUDA tensors (on ROCm, HIP devices):
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
 import os
@@ -53,11 +54,18 @@ NVFP4_MAX_GROUPS = 256
 EXPORTED = ("nvfp4_compute_amax", "nvfp4_quantize", "nvfp4_dequantize", "nvfp4_last_error",
             "nvfp4_workspace_bytes", "nvfp4_swizzle_scales", "nvfp4_swizzled_scales_bytes", "nvfp4_quantize_grouped",
             "nvfp4_debug_rht_colwise", "nvfp4_debug_e2m1_pack", "nvfp4_debug_set_wait_ticks",
-            "nvfp4_quantize_noalloc", "nvfp4_debug_set_rht_unit", "nvfp4_debug_set_resident_variant")
+            "nvfp4_quantize_noalloc", "nvfp4_debug_set_rht_unit", "nvfp4_debug_set_resident_variant",
+            "nvfp4_expert_rows", "nvfp4_expert_sort_workspace_bytes", "nvfp4_expert_sort", "nvfp4_expert_gather",
+            "nvfp4_expert_combine", "nvfp4_expert_combine_grad", "nvfp4_fp8_pitch", "nvfp4_fp8_quantize",
+            "nvfp4_fp8_matmul", "nvfp4_fp8_matmul_grouped", "nvfp4_fp8_matmul_grouped_k")
 
 
 class nvfp4_out_t(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("amax", ctypes.c_void_p)]
+
+
+class nvfp4_fp8_t(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
 
 
 class nvfp4_config_t(ctypes.Structure):
@@ -137,6 +145,29 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
     lib.nvfp4_debug_set_rht_unit.argtypes = [U32]
     lib.nvfp4_debug_set_resident_variant.restype = I
     lib.nvfp4_debug_set_resident_variant.argtypes = [U32]
+    FP8 = ctypes.POINTER(nvfp4_fp8_t)
+    lib.nvfp4_expert_rows.restype = ctypes.c_uint64
+    lib.nvfp4_expert_rows.argtypes = [I64, I64, I64, I64]
+    lib.nvfp4_expert_sort_workspace_bytes.restype = ctypes.c_uint64
+    lib.nvfp4_expert_sort_workspace_bytes.argtypes = [I64, I64, I64]
+    lib.nvfp4_expert_sort.restype = I
+    lib.nvfp4_expert_sort.argtypes = [P, U32, I64, I64, I64, I64, I64, P, P, P, P, P, P]
+    lib.nvfp4_expert_gather.restype = I
+    lib.nvfp4_expert_gather.argtypes = [P, I, I64, I64, I64, P, I64, P, P]
+    lib.nvfp4_expert_combine.restype = I
+    lib.nvfp4_expert_combine.argtypes = [P, I, I64, I64, I64, P, I64, P, P, P]
+    lib.nvfp4_expert_combine_grad.restype = I
+    lib.nvfp4_expert_combine_grad.argtypes = [P, P, I, I64, I64, I64, P, P, I64, P, P, P, P]
+    lib.nvfp4_fp8_pitch.restype = ctypes.c_uint64
+    lib.nvfp4_fp8_pitch.argtypes = [I64]
+    lib.nvfp4_fp8_quantize.restype = I
+    lib.nvfp4_fp8_quantize.argtypes = [P, I, I64, I64, I64, P, I64, I64, U32, FP8, FP8, P]
+    lib.nvfp4_fp8_matmul.restype = I
+    lib.nvfp4_fp8_matmul.argtypes = [FP8, FP8, I64, I64, I64, U32, P, I, P]
+    lib.nvfp4_fp8_matmul_grouped.restype = I
+    lib.nvfp4_fp8_matmul_grouped.argtypes = [FP8, FP8, P, I64, I64, I64, I64, P, I, P]
+    lib.nvfp4_fp8_matmul_grouped_k.restype = I
+    lib.nvfp4_fp8_matmul_grouped_k.argtypes = [FP8, FP8, P, I64, I64, I64, I64, P, I, P]
     _lib = lib
     return lib
 
@@ -425,3 +456,284 @@ def quantize(x: torch.Tensor, *, rowwise=True, columnwise=True, cfg: Optional[nv
         cfg.workspace = ws.data_ptr()
     nvfp4_quantize(x, row, col, cfg, stream)
     return row, col
+
+
+# ---- expert layers: tokens by expert, block-scaled FP8, products -------------
+#
+# Outputs are allocated on the stream that the call runs on, so a caller who
+# passes `stream` may let go of them as with any tensor made under it.
+
+FP8_BLOCK = 128
+
+
+@dataclasses.dataclass
+class ExpertPlan:
+    """Where expert_sort put each slot (choice j of token t is slot t * topk + j).
+
+    slot_rows [tokens][topk] the slot's sorted row (-1: dropped); row_slots
+    [rows] the row's slot (-1: padding); offsets [experts + 1] each expert's
+    first row, a multiple of align; counts [experts] its slots. All int32, on
+    the device: nothing is read back to the host."""
+    slot_rows: torch.Tensor
+    row_slots: torch.Tensor
+    offsets: torch.Tensor
+    counts: torch.Tensor
+    align: int
+
+    @property
+    def tokens(self) -> int:
+        return self.slot_rows.shape[0]
+
+    @property
+    def topk(self) -> int:
+        return self.slot_rows.shape[1]
+
+    @property
+    def experts(self) -> int:
+        return self.counts.shape[0]
+
+    @property
+    def rows(self) -> int:
+        return self.row_slots.shape[0]
+
+
+@dataclasses.dataclass
+class Fp8Tensor:
+    """n rows of k values in block-scaled FP8, or a batch of such matrices.
+
+    data float8_e4m3fn [..][n][pitch(k)], zero from k on; scales float32
+    [..][ceil(k / 128)][n] (1x128 blocks) or [..][ceil(k / 128)][ceil(n / 128)]
+    (block_2d: 128x128 blocks)."""
+    data: torch.Tensor
+    scales: torch.Tensor
+    n: int
+    k: int
+    block_2d: bool = False
+
+    def as_c(self) -> nvfp4_fp8_t:
+        return nvfp4_fp8_t(self.data.data_ptr(), self.scales.data_ptr())
+
+
+def _is(t, dtype, shape, device) -> bool:
+    return (isinstance(t, torch.Tensor) and t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.is_contiguous()
+            and t.device == device)
+
+
+def _want(t, dtype, shape, device, what: str) -> None:
+    if not _is(t, dtype, shape, device):
+        got = f"{t.dtype} {tuple(t.shape)} on {t.device}" if isinstance(t, torch.Tensor) else type(t).__name__
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got {got}")
+
+
+def _on(x: torch.Tensor, what: str) -> torch.device:
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or not x.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous CUDA tensor")
+    return x.device
+
+
+def _as_stream(stream, device):
+    """The context that a call's outputs are allocated in, and the stream's handle."""
+    if stream is None:
+        return contextlib.nullcontext(), ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device)
+    return torch.cuda.stream(s), ctypes.c_void_p(s.cuda_stream)
+
+
+def _want_plan(plan: ExpertPlan, device) -> None:
+    i32 = torch.int32
+    if plan.slot_rows.dim() != 2 or plan.row_slots.dim() != 1 or plan.counts.dim() != 1:
+        raise ValueError("a plan has slot_rows [tokens][topk], row_slots [rows] and counts [experts]")
+    _want(plan.slot_rows, i32, plan.slot_rows.shape, device, "plan.slot_rows")
+    _want(plan.row_slots, i32, plan.row_slots.shape, device, "plan.row_slots")
+    _want(plan.counts, i32, plan.counts.shape, device, "plan.counts")
+    _want(plan.offsets, i32, (plan.experts + 1,), device, "plan.offsets")
+
+
+def expert_sort(ids: torch.Tensor, experts: int, *, align: int = FP8_BLOCK, rows: Optional[int] = None,
+                stream=None) -> ExpertPlan:
+    """Sort the slots of a router (ids int32 or int64 [tokens][topk]; an id
+    outside 0 .. experts - 1 drops its slot) by expert, each expert's rows
+    starting at a multiple of align (a power of two up to 128). rows: rows of
+    the sorted matrix, by default as many as any ids could need."""
+    dev = _on(ids, "ids")
+    if ids.dim() != 2 or ids.dtype not in (torch.int32, torch.int64):
+        raise ValueError("ids must be int32 or int64 [tokens][topk]")
+    lib = load()
+    tokens, topk = ids.shape
+    if rows is None:
+        rows = int(lib.nvfp4_expert_rows(tokens, topk, experts, align))
+    ctx, s = _as_stream(stream, dev)
+    with ctx:
+        n = lib.nvfp4_expert_sort_workspace_bytes(tokens, topk, experts)
+        slot_rows = torch.empty((tokens, topk), dtype=torch.int32, device=dev)
+        row_slots = torch.empty((max(rows, 0),), dtype=torch.int32, device=dev)
+        offsets = torch.empty((max(experts, 0) + 1,), dtype=torch.int32, device=dev)
+        counts = torch.empty((max(experts, 0),), dtype=torch.int32, device=dev)
+        ws = torch.empty((n,), dtype=torch.uint8, device=dev) if n else None
+        _check(lib.nvfp4_expert_sort(_ptr(ids), ids.element_size(), tokens, topk, experts, align, rows, _ptr(slot_rows),
+                                     _ptr(row_slots), _ptr(offsets), _ptr(counts), _ptr(ws), s))
+    return ExpertPlan(slot_rows, row_slots, offsets, counts, align)
+
+
+def expert_gather(x: torch.Tensor, plan: ExpertPlan, *, stream=None) -> torch.Tensor:
+    """x [tokens][cols] to the sorted rows [rows][cols], zeros in padding."""
+    dev = _on(x, "x")
+    _want_plan(plan, dev)
+    if x.dim() != 2 or x.shape[0] != plan.tokens:
+        raise ValueError(f"x must be [{plan.tokens}][cols], got {tuple(x.shape)}")
+    code = _dtype_code(x)
+    ctx, s = _as_stream(stream, dev)
+    with ctx:
+        y = torch.empty((plan.rows, x.shape[1]), dtype=x.dtype, device=dev)
+        _check(load().nvfp4_expert_gather(_ptr(x), code, plan.tokens, plan.topk, x.shape[1], _ptr(plan.row_slots), plan.rows,
+                                          _ptr(y), s))
+    return y
+
+
+def expert_combine(y: torch.Tensor, plan: ExpertPlan, weights: Optional[torch.Tensor] = None, *, stream=None) -> torch.Tensor:
+    """The sorted rows y [rows][cols] back to tokens [tokens][cols], summed
+    over each token's slots with weights (float32 [tokens][topk]; None: ones).
+    Padding rows and dropped slots are not read."""
+    dev = _on(y, "y")
+    _want_plan(plan, dev)
+    if y.dim() != 2 or y.shape[0] != plan.rows:
+        raise ValueError(f"y must be [{plan.rows}][cols], got {tuple(y.shape)}")
+    if weights is not None:
+        _want(weights, torch.float32, (plan.tokens, plan.topk), dev, "weights")
+    code = _dtype_code(y)
+    ctx, s = _as_stream(stream, dev)
+    with ctx:
+        out = torch.empty((plan.tokens, y.shape[1]), dtype=y.dtype, device=dev)
+        _check(load().nvfp4_expert_combine(_ptr(y), code, plan.tokens, plan.topk, y.shape[1], _ptr(plan.slot_rows), plan.rows,
+                                           _ptr(weights), _ptr(out), s))
+    return out
+
+
+def expert_gather_grad(dy: torch.Tensor, plan: ExpertPlan, *, stream=None) -> torch.Tensor:
+    """The gradient of expert_gather's x from that of its sorted rows."""
+    return expert_combine(dy, plan, None, stream=stream)
+
+
+def expert_combine_grad(dout: torch.Tensor, y: torch.Tensor, plan: ExpertPlan, weights: torch.Tensor, *, stream=None):
+    """The gradients (dy [rows][cols], dweights float32 [tokens][topk]) of
+    expert_combine(y, plan, weights) from dout [tokens][cols]."""
+    dev = _on(dout, "dout")
+    _want_plan(plan, dev)
+    if dout.dim() != 2 or dout.shape[0] != plan.tokens:
+        raise ValueError(f"dout must be [{plan.tokens}][cols], got {tuple(dout.shape)}")
+    cols = dout.shape[1]
+    _want(y, dout.dtype, (plan.rows, cols), dev, "y")
+    _want(weights, torch.float32, (plan.tokens, plan.topk), dev, "weights")
+    code = _dtype_code(dout)
+    ctx, s = _as_stream(stream, dev)
+    with ctx:
+        dy = torch.empty((plan.rows, cols), dtype=dout.dtype, device=dev)
+        dw = torch.empty((plan.tokens, plan.topk), dtype=torch.float32, device=dev)
+        _check(load().nvfp4_expert_combine_grad(_ptr(dout), _ptr(y), code, plan.tokens, plan.topk, cols, _ptr(plan.slot_rows),
+                                                _ptr(plan.row_slots), plan.rows, _ptr(weights), _ptr(dy), _ptr(dw), s))
+    return dy, dw
+
+
+def nvfp4_fp8_pitch(k: int) -> int:
+    return int(load().nvfp4_fp8_pitch(k))
+
+
+def _blocks(n: int) -> int:
+    return (n + FP8_BLOCK - 1) // FP8_BLOCK
+
+
+def fp8_quantize(x: torch.Tensor, *, rowwise=True, columnwise=False, block_2d=False, plan: Optional[ExpertPlan] = None,
+                 stream=None):
+    """Quantize x [R][C], or a batch [B][R][C], to block-scaled FP8 (1x128
+    blocks, or 128x128 with block_2d). Returns (row, col): x itself with k = C,
+    and its transpose with k = R; None for one not asked for. With a plan, x
+    is [tokens][C] and the matrix is expert_gather(x, plan)."""
+    dev = _on(x, "x")
+    if x.dim() != 2 and (x.dim() != 3 or plan is not None):
+        raise ValueError("x must be [R][C] or, without a plan, [B][R][C]")
+    code = _dtype_code(x)
+    lead, batch = tuple(x.shape[:-2]), x.shape[0] if x.dim() == 3 else 1
+    rows, cols = x.shape[-2:]
+    slots, tokens, topk = None, 0, 1
+    if plan is not None:
+        _want_plan(plan, dev)
+        if rows != plan.tokens:
+            raise ValueError(f"x must be [{plan.tokens}][cols], got {tuple(x.shape)}")
+        slots, tokens, topk, rows = plan.row_slots, plan.tokens, plan.topk, plan.rows
+    ctx, s = _as_stream(stream, dev)
+
+    def empty(n, k):
+        return Fp8Tensor(torch.empty((*lead, n, _blocks(k) * FP8_BLOCK), dtype=torch.float8_e4m3fn, device=dev),
+                         torch.empty((*lead, _blocks(k), _blocks(n) if block_2d else n), dtype=torch.float32, device=dev),
+                         n, k, bool(block_2d))
+
+    with ctx:
+        row = empty(rows, cols) if rowwise else None
+        col = empty(cols, rows) if columnwise else None
+        r, c = row.as_c() if row is not None else None, col.as_c() if col is not None else None
+        _check(load().nvfp4_fp8_quantize(_ptr(x), code, batch, rows, cols, _ptr(slots), tokens, topk, int(block_2d), r, c, s))
+    return row, col
+
+
+def _want_fp8(q: Fp8Tensor, lead, n: int, k: int, block_2d: bool, device, what: str) -> None:
+    if q.n != n or q.k != k or bool(q.block_2d) != block_2d:
+        raise ValueError(f"{what} must have {n} rows of {k} values in {'128x128' if block_2d else '1x128'} blocks, got "
+                         f"{q.n} x {q.k}, block_2d={q.block_2d}")
+    kb = _blocks(k)
+    _want(q.data, torch.float8_e4m3fn, (*lead, n, kb * FP8_BLOCK), device, f"{what} data")
+    _want(q.scales, torch.float32, (*lead, kb, _blocks(n) if block_2d else n), device, f"{what} scales")
+
+
+def _out_code(dtype) -> int:
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"the output type must be bfloat16 or float32, got {dtype}")
+    return NVFP4_IN_BF16 if dtype == torch.bfloat16 else NVFP4_IN_FP32
+
+
+def fp8_matmul(a: Fp8Tensor, b: Fp8Tensor, *, out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    """a b^T [a.n][b.n]; a in 1x128 blocks, b in 1x128 or 128x128 blocks."""
+    dev = _on(a.data, "operand a")
+    code = _out_code(out_dtype)
+    _want_fp8(a, (), a.n, a.k, False, dev, "operand a")
+    _want_fp8(b, (), b.n, a.k, bool(b.block_2d), dev, "operand b")
+    ctx, s = _as_stream(stream, dev)
+    with ctx:
+        d = torch.empty((a.n, b.n), dtype=out_dtype, device=dev)
+        _check(load().nvfp4_fp8_matmul(a.as_c(), b.as_c(), a.n, b.n, a.k, int(b.block_2d), _ptr(d), code, s))
+    return d
+
+
+def fp8_matmul_grouped(a: Fp8Tensor, b: Fp8Tensor, plan: ExpertPlan, *, out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    """Each expert's rows of a (1x128 blocks, plan.rows rows) times its matrix
+    of the batch b ([experts], 128x128 blocks): [plan.rows][b.n], zeros past
+    the last expert's rows."""
+    dev = _on(a.data, "operand a")
+    code = _out_code(out_dtype)
+    _want_plan(plan, dev)
+    _want_fp8(a, (), plan.rows, a.k, False, dev, "operand a")
+    _want_fp8(b, (plan.experts,), b.n, a.k, True, dev, "operand b")
+    ctx, s = _as_stream(stream, dev)
+    with ctx:
+        d = torch.empty((plan.rows, b.n), dtype=out_dtype, device=dev)
+        _check(load().nvfp4_fp8_matmul_grouped(a.as_c(), b.as_c(), _ptr(plan.offsets), plan.experts, plan.rows, b.n, a.k,
+                                               _ptr(d), code, s))
+    return d
+
+
+def fp8_matmul_grouped_k(a: Fp8Tensor, b: Fp8Tensor, plan: ExpertPlan, *, out_dtype=torch.float32, stream=None) -> torch.Tensor:
+    """Per expert, a b^T over its rows, which are k here: [experts][a.n][b.n],
+    zeros for an expert without rows. a and b are column-wise orientations of
+    sorted rows (k = plan.rows, 1x128 blocks) and the plan's align is 128."""
+    dev = _on(a.data, "operand a")
+    code = _out_code(out_dtype)
+    _want_plan(plan, dev)
+    if plan.align != FP8_BLOCK:
+        raise ValueError(f"the plan must be aligned to {FP8_BLOCK} rows, got {plan.align}")
+    _want_fp8(a, (), a.n, plan.rows, False, dev, "operand a")
+    _want_fp8(b, (), b.n, plan.rows, False, dev, "operand b")
+    ctx, s = _as_stream(stream, dev)
+    with ctx:
+        d = torch.empty((plan.experts, a.n, b.n), dtype=out_dtype, device=dev)
+        _check(load().nvfp4_fp8_matmul_grouped_k(a.as_c(), b.as_c(), _ptr(plan.offsets), plan.experts, a.n, b.n, plan.rows,
+                                                 _ptr(d), code, s))
+    return d

@@ -557,3 +557,274 @@ extern "C" nvfp4_status_t nvfp4_debug_e2m1_pack(const float *v, const uint32_t *
                                              static_cast<hipStream_t>(stream)),
                     "debug e2m1 launch");
 }
+
+// ---------------------------------------------------------------------------
+// Expert layers and block-scaled FP8.
+// ---------------------------------------------------------------------------
+namespace {
+
+constexpr int64_t kIndexLimit = int64_t{1} << 31;  // rows, slots and grids stay below it
+constexpr int64_t kFp8KLimit = int64_t{1} << 23;   // 256 rows of it stay within 32-bit offsets
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+nvfp4_status_t check_dtype(nvfp4_dtype_t dtype, const char *what) {
+  if (dtype == NVFP4_IN_BF16 || dtype == NVFP4_IN_FP32) return NVFP4_OK;
+  return fail(NVFP4_ERR_UNSUPPORTED, "unknown %s type %d", what, static_cast<int>(dtype));
+}
+
+// A buffer that must be there (unless it is empty) and aligned.
+nvfp4_status_t check_buffer(const void *p, uintptr_t alignment, bool empty, const char *what) {
+  if (p == nullptr) return empty ? NVFP4_OK : fail(NVFP4_ERR_NULL, "%s is NULL", what);
+  if (!aligned(p, alignment)) return fail(NVFP4_ERR_ALIGN, "%s is not %d-byte aligned", what, static_cast<int>(alignment));
+  return NVFP4_OK;
+}
+
+nvfp4_status_t check_slots(int64_t tokens, int64_t topk) {
+  if (tokens < 0 || topk < 1) return fail(NVFP4_ERR_SHAPE, "tokens = %lld, topk = %lld", (long long)tokens, (long long)topk);
+  if (product_at_least(tokens, topk, kIndexLimit)) return fail(NVFP4_ERR_SHAPE, "tokens * topk must be below 2^31");
+  return NVFP4_OK;
+}
+
+nvfp4_status_t check_sort(int64_t tokens, int64_t topk, int64_t experts, int64_t align) {
+  const nvfp4_status_t st = check_slots(tokens, topk);
+  if (st != NVFP4_OK) return st;
+  if (experts < 1 || experts > NVFP4_MAX_GROUPS)
+    return fail(NVFP4_ERR_SHAPE, "experts = %lld must be in [1, %d]", (long long)experts, NVFP4_MAX_GROUPS);
+  if (align < 1 || align > 128 || (align & (align - 1)) != 0)
+    return fail(NVFP4_ERR_UNSUPPORTED, "align = %lld must be a power of two up to 128", (long long)align);
+  return NVFP4_OK;
+}
+
+uint64_t sorted_rows(int64_t tokens, int64_t topk, int64_t experts, int64_t align) {
+  const int64_t slots = tokens * topk, used = experts < slots ? experts : slots;
+  return static_cast<uint64_t>((slots + used * (align - 1)) / align * align);
+}
+
+// Shapes and maps of the calls that move rows; the grids that they launch.
+nvfp4_status_t check_rows(nvfp4_dtype_t dtype, int64_t tokens, int64_t topk, int64_t cols, int64_t rows) {
+  nvfp4_status_t st = check_dtype(dtype, "element");
+  if (st != NVFP4_OK || (st = check_slots(tokens, topk)) != NVFP4_OK) return st;
+  if (cols < 0 || cols >= kIndexLimit) return fail(NVFP4_ERR_SHAPE, "cols = %lld out of range", (long long)cols);
+  if (rows < 0 || rows >= kIndexLimit) return fail(NVFP4_ERR_SHAPE, "rows = %lld out of range", (long long)rows);
+  if (product_at_least(tokens, ceil_div(cols, 256), kIndexLimit))
+    return fail(NVFP4_ERR_SHAPE, "tokens * cols is too large for one launch");
+  return NVFP4_OK;
+}
+
+nvfp4_status_t check_fp8(const nvfp4_fp8_t *q, bool empty, const char *what) {
+  if (q == nullptr) return fail(NVFP4_ERR_NULL, "%s is NULL", what);
+  nvfp4_status_t st = check_buffer(q->data, 16, empty, what);
+  return st != NVFP4_OK ? st : check_buffer(q->scales, 4, empty, what);
+}
+
+// The checks that the three products share, and their launch. rows: of a.
+nvfp4_status_t matmul(const nvfp4_fp8_t *a, const nvfp4_fp8_t *b, int64_t rows, int64_t n, int64_t k, bool b_block_2d,
+                      uint32_t mode, const int32_t *offsets, int64_t groups, void *d, nvfp4_dtype_t d_dtype, void *stream) {
+  nvfp4_status_t st = check_dtype(d_dtype, "output");
+  if (st != NVFP4_OK) return st;
+  if (rows < 0 || n < 0 || k < 0 || rows >= kIndexLimit || n >= kIndexLimit)
+    return fail(NVFP4_ERR_SHAPE, "a product of %lld x %lld x %lld", (long long)rows, (long long)n, (long long)k);
+  if (k >= kFp8KLimit) return fail(NVFP4_ERR_SHAPE, "k = %lld must be below 2^23", (long long)k);
+  if (mode != nvfp4::kDense && (groups < 1 || groups > NVFP4_MAX_GROUPS))
+    return fail(NVFP4_ERR_SHAPE, "groups = %lld must be in [1, %d]", (long long)groups, NVFP4_MAX_GROUPS);
+  const int64_t row_tiles = mode == nvfp4::kGroupedK ? ceil_div(rows, 16) * groups : ceil_div(rows, 16) + groups + 1;
+  if (product_at_least(row_tiles, ceil_div(n, 16), kIndexLimit))
+    return fail(NVFP4_ERR_SHAPE, "an output of %lld x %lld is too large for one launch", (long long)rows, (long long)n);
+  const bool empty = rows == 0 || n == 0;
+  if ((st = check_fp8(a, empty || k == 0, "operand a")) != NVFP4_OK) return st;
+  if ((st = check_fp8(b, empty || k == 0, "operand b")) != NVFP4_OK) return st;
+  if ((st = check_buffer(d, 16, empty, "the output")) != NVFP4_OK) return st;
+  if (mode != nvfp4::kDense && (st = check_buffer(offsets, 4, false, "offsets")) != NVFP4_OK) return st;
+  if (empty) return NVFP4_OK;
+  nvfp4::Fp8Matmul p{};
+  p.a = a->data;
+  p.sa = a->scales;
+  p.b = b->data;
+  p.sb = b->scales;
+  p.d = d;
+  p.m = static_cast<uint32_t>(rows);
+  p.n = static_cast<uint32_t>(n);
+  p.kblocks = static_cast<uint32_t>(ceil_div(k, nvfp4::kFp8Block));
+  p.sa_stride = p.m;
+  p.sb_stride = b_block_2d ? static_cast<uint32_t>(ceil_div(n, nvfp4::kFp8Block)) : p.n;
+  p.b_block_2d = b_block_2d;
+  p.out_fp32 = d_dtype == NVFP4_IN_FP32;
+  p.mode = mode;
+  p.offsets = offsets;
+  p.groups = static_cast<uint32_t>(groups);
+  return hip_status(nvfp4::launch_fp8_matmul(p, static_cast<hipStream_t>(stream)), "FP8 product launch");
+}
+
+}  // namespace
+
+extern "C" uint64_t nvfp4_expert_rows(int64_t tokens, int64_t topk, int64_t experts, int64_t align) {
+  return check_sort(tokens, topk, experts, align) == NVFP4_OK ? sorted_rows(tokens, topk, experts, align) : 0;
+}
+
+extern "C" uint64_t nvfp4_expert_sort_workspace_bytes(int64_t tokens, int64_t topk, int64_t experts) {
+  if (check_sort(tokens, topk, experts, 1) != NVFP4_OK) return 0;
+  return 4 * nvfp4::expert_sort_workspace_words(static_cast<uint64_t>(tokens * topk), static_cast<uint32_t>(experts));
+}
+
+extern "C" nvfp4_status_t nvfp4_expert_sort(const void *ids, uint32_t id_bytes, int64_t tokens, int64_t topk, int64_t experts,
+                                            int64_t align, int64_t rows, int32_t *slot_rows, int32_t *row_slots,
+                                            int32_t *offsets, int32_t *counts, void *workspace, void *stream) {
+  nvfp4_status_t st = check_sort(tokens, topk, experts, align);
+  if (st != NVFP4_OK) return st;
+  if (id_bytes != 4 && id_bytes != 8) return fail(NVFP4_ERR_UNSUPPORTED, "ids of %u bytes", id_bytes);
+  const int64_t need = static_cast<int64_t>(sorted_rows(tokens, topk, experts, align));
+  if (rows < need || rows >= kIndexLimit)
+    return fail(NVFP4_ERR_SHAPE, "rows = %lld must be at least %lld and below 2^31", (long long)rows, (long long)need);
+  const bool none = tokens == 0;
+  if ((st = check_buffer(ids, id_bytes, none, "ids")) != NVFP4_OK) return st;
+  if ((st = check_buffer(slot_rows, 4, none, "slot_rows")) != NVFP4_OK) return st;
+  if ((st = check_buffer(row_slots, 4, rows == 0, "row_slots")) != NVFP4_OK) return st;
+  if ((st = check_buffer(offsets, 4, false, "offsets")) != NVFP4_OK) return st;
+  if ((st = check_buffer(counts, 4, false, "counts")) != NVFP4_OK) return st;
+  const uint64_t words = nvfp4::expert_sort_workspace_words(static_cast<uint64_t>(tokens * topk), static_cast<uint32_t>(experts));
+  if ((st = check_buffer(workspace, 4, words == 0, "the workspace")) != NVFP4_OK) return st;
+  nvfp4::ExpertSort p{};
+  p.ids = ids;
+  p.wide = id_bytes == 8;
+  p.slots = static_cast<uint32_t>(tokens * topk);
+  p.experts = static_cast<uint32_t>(experts);
+  p.align_log2 = static_cast<uint32_t>(__builtin_ctzll(static_cast<uint64_t>(align)));
+  p.rows = static_cast<uint32_t>(rows);
+  p.slot_rows = slot_rows;
+  p.row_slots = row_slots;
+  p.offsets = offsets;
+  p.counts = counts;
+  p.workspace = static_cast<uint32_t *>(workspace);
+  return hip_status(nvfp4::launch_expert_sort(p, static_cast<hipStream_t>(stream)), "expert sort launch");
+}
+
+extern "C" nvfp4_status_t nvfp4_expert_gather(const void *x, nvfp4_dtype_t dtype, int64_t tokens, int64_t topk, int64_t cols,
+                                              const int32_t *row_slots, int64_t rows, void *y, void *stream) {
+  nvfp4_status_t st = check_rows(dtype, tokens, topk, cols, rows);
+  if (st != NVFP4_OK) return st;
+  const bool empty = rows == 0 || cols == 0;
+  if ((st = check_buffer(x, 16, empty || tokens == 0, "x")) != NVFP4_OK) return st;
+  if ((st = check_buffer(row_slots, 4, empty, "row_slots")) != NVFP4_OK) return st;
+  if ((st = check_buffer(y, 16, empty, "y")) != NVFP4_OK) return st;
+  if (empty) return NVFP4_OK;
+  nvfp4::ExpertRows p{};
+  p.x = x;
+  p.row_slots = row_slots;
+  p.tokens = static_cast<uint32_t>(tokens);
+  p.topk = static_cast<uint32_t>(topk);
+  p.cols = static_cast<uint32_t>(cols);
+  p.rows = static_cast<uint32_t>(rows);
+  p.out = y;
+  return hip_status(nvfp4::launch_expert_gather(p, dtype, static_cast<hipStream_t>(stream)), "expert gather launch");
+}
+
+extern "C" nvfp4_status_t nvfp4_expert_combine(const void *y, nvfp4_dtype_t dtype, int64_t tokens, int64_t topk, int64_t cols,
+                                               const int32_t *slot_rows, int64_t rows, const float *weights, void *out,
+                                               void *stream) {
+  nvfp4_status_t st = check_rows(dtype, tokens, topk, cols, rows);
+  if (st != NVFP4_OK) return st;
+  const bool empty = tokens == 0 || cols == 0;
+  if ((st = check_buffer(y, 16, empty || rows == 0, "y")) != NVFP4_OK) return st;
+  if ((st = check_buffer(slot_rows, 4, empty, "slot_rows")) != NVFP4_OK) return st;
+  if ((st = check_buffer(weights, 4, true, "weights")) != NVFP4_OK) return st;
+  if ((st = check_buffer(out, 16, empty, "the output")) != NVFP4_OK) return st;
+  if (empty) return NVFP4_OK;
+  nvfp4::ExpertRows p{};
+  p.x = y;
+  p.slot_rows = slot_rows;
+  p.weights = weights;
+  p.tokens = static_cast<uint32_t>(tokens);
+  p.topk = static_cast<uint32_t>(topk);
+  p.cols = static_cast<uint32_t>(cols);
+  p.rows = static_cast<uint32_t>(rows);
+  p.out = out;
+  return hip_status(nvfp4::launch_expert_combine(p, dtype, static_cast<hipStream_t>(stream)), "expert combine launch");
+}
+
+extern "C" nvfp4_status_t nvfp4_expert_combine_grad(const void *dout, const void *y, nvfp4_dtype_t dtype, int64_t tokens,
+                                                    int64_t topk, int64_t cols, const int32_t *slot_rows,
+                                                    const int32_t *row_slots, int64_t rows, const float *weights, void *dy,
+                                                    float *dweights, void *stream) {
+  nvfp4_status_t st = check_rows(dtype, tokens, topk, cols, rows);
+  if (st != NVFP4_OK) return st;
+  const bool no_tokens = tokens == 0, no_rows = rows == 0 || cols == 0;
+  if ((st = check_buffer(dout, 16, no_tokens || cols == 0, "dout")) != NVFP4_OK) return st;
+  if ((st = check_buffer(y, 16, no_tokens || no_rows, "y")) != NVFP4_OK) return st;
+  if ((st = check_buffer(slot_rows, 4, no_tokens, "slot_rows")) != NVFP4_OK) return st;
+  if ((st = check_buffer(row_slots, 4, no_rows, "row_slots")) != NVFP4_OK) return st;
+  if ((st = check_buffer(weights, 4, no_tokens, "weights")) != NVFP4_OK) return st;
+  if ((st = check_buffer(dy, 16, no_rows, "dy")) != NVFP4_OK) return st;
+  if ((st = check_buffer(dweights, 4, no_tokens, "dweights")) != NVFP4_OK) return st;
+  if (no_tokens && no_rows) return NVFP4_OK;
+  nvfp4::ExpertRows p{};
+  p.x = dout;
+  p.y = y;
+  p.slot_rows = slot_rows;
+  p.row_slots = row_slots;
+  p.weights = weights;
+  p.tokens = static_cast<uint32_t>(tokens);
+  p.topk = static_cast<uint32_t>(topk);
+  p.cols = static_cast<uint32_t>(cols);
+  p.rows = no_rows ? 0u : static_cast<uint32_t>(rows);
+  p.out = dy;
+  p.dweights = dweights;
+  return hip_status(nvfp4::launch_expert_combine_grad(p, dtype, static_cast<hipStream_t>(stream)), "expert combine gradient launch");
+}
+
+extern "C" uint64_t nvfp4_fp8_pitch(int64_t k) {
+  return k <= 0 ? 0 : (static_cast<uint64_t>(k) + nvfp4::kFp8Block - 1) / nvfp4::kFp8Block * nvfp4::kFp8Block;
+}
+
+extern "C" nvfp4_status_t nvfp4_fp8_quantize(const void *x, nvfp4_dtype_t dtype, int64_t batch, int64_t rows, int64_t cols,
+                                             const int32_t *row_slots, int64_t tokens, int64_t topk, uint32_t block_2d,
+                                             const nvfp4_fp8_t *row, const nvfp4_fp8_t *col, void *stream) {
+  nvfp4_status_t st = check_dtype(dtype, "input");
+  if (st != NVFP4_OK) return st;
+  if (batch < 0 || rows < 0 || cols < 0 || batch >= kIndexLimit || rows >= kIndexLimit || cols >= kIndexLimit)
+    return fail(NVFP4_ERR_SHAPE, "a batch of %lld matrices of %lld x %lld", (long long)batch, (long long)rows, (long long)cols);
+  const int64_t tiles = ceil_div(rows, nvfp4::kFp8Block) * ceil_div(cols, nvfp4::kFp8Block);
+  if (product_at_least(tiles, batch, kIndexLimit)) return fail(NVFP4_ERR_SHAPE, "2^31 or more blocks of 128 x 128");
+  if (row == nullptr && col == nullptr) return fail(NVFP4_ERR_NULL, "neither a row-wise nor a column-wise output");
+  if (row_slots != nullptr) {
+    if (batch != 1) return fail(NVFP4_ERR_UNSUPPORTED, "row_slots takes a batch of one matrix");
+    if (!aligned(row_slots, 4)) return fail(NVFP4_ERR_ALIGN, "row_slots is not 4-byte aligned");
+    if ((st = check_slots(tokens, topk)) != NVFP4_OK) return st;
+  }
+  const bool empty = batch * rows * cols == 0;
+  if ((st = check_buffer(x, 16, empty || (row_slots && tokens == 0), "x")) != NVFP4_OK) return st;
+  if (row && (st = check_fp8(row, empty, "the row-wise output")) != NVFP4_OK) return st;
+  if (col && (st = check_fp8(col, empty, "the column-wise output")) != NVFP4_OK) return st;
+  if (empty) return NVFP4_OK;
+  nvfp4::Fp8Quantize p{};
+  p.x = x;
+  p.batch = static_cast<uint32_t>(batch);
+  p.rows = static_cast<uint32_t>(rows);
+  p.cols = static_cast<uint32_t>(cols);
+  p.row_slots = row_slots;
+  p.slots = row_slots ? static_cast<uint32_t>(tokens * topk) : 0;
+  p.topk = row_slots ? static_cast<uint32_t>(topk) : 1;
+  p.row_data = row ? row->data : nullptr;
+  p.row_scales = row ? row->scales : nullptr;
+  p.col_data = col ? col->data : nullptr;
+  p.col_scales = col ? col->scales : nullptr;
+  return hip_status(nvfp4::launch_fp8_quantize(p, dtype, block_2d != 0, static_cast<hipStream_t>(stream)),
+                    "FP8 quantize launch");
+}
+
+extern "C" nvfp4_status_t nvfp4_fp8_matmul(const nvfp4_fp8_t *a, const nvfp4_fp8_t *b, int64_t m, int64_t n, int64_t k,
+                                           uint32_t b_block_2d, void *d, nvfp4_dtype_t d_dtype, void *stream) {
+  return matmul(a, b, m, n, k, b_block_2d != 0, nvfp4::kDense, nullptr, 0, d, d_dtype, stream);
+}
+
+extern "C" nvfp4_status_t nvfp4_fp8_matmul_grouped(const nvfp4_fp8_t *a, const nvfp4_fp8_t *b, const int32_t *offsets,
+                                                   int64_t groups, int64_t rows, int64_t n, int64_t k, void *d,
+                                                   nvfp4_dtype_t d_dtype, void *stream) {
+  return matmul(a, b, rows, n, k, true, nvfp4::kGroupedRows, offsets, groups, d, d_dtype, stream);
+}
+
+extern "C" nvfp4_status_t nvfp4_fp8_matmul_grouped_k(const nvfp4_fp8_t *a, const nvfp4_fp8_t *b, const int32_t *offsets,
+                                                     int64_t groups, int64_t m, int64_t n, int64_t k, void *d,
+                                                     nvfp4_dtype_t d_dtype, void *stream) {
+  return matmul(a, b, m, n, k, false, nvfp4::kGroupedK, offsets, groups, d, d_dtype, stream);
+}

@@ -197,6 +197,57 @@ hipError_t launch_dequant(const uint8_t *data, const uint8_t *scales, const floa
 // zero-padded compact -> GEMM-swizzled scales; out holds swizzled_scales_bytes()
 uint64_t swizzled_scales_bytes(uint64_t rows, uint64_t scale_cols);
 hipError_t launch_swizzle(const uint8_t *compact, uint32_t rows, uint32_t scale_cols, uint8_t *out, hipStream_t s);
+
+// Tokens by expert. Validated by the caller: tokens * topk < 2^31, rows <
+// 2^31, cols < 2^31, experts in 1 .. kMaxGroups, grids below 2^31 blocks.
+struct ExpertSort {
+  const void *ids;
+  uint32_t wide;  // 64-bit ids
+  uint32_t slots, experts, align_log2, rows;
+  int32_t *slot_rows, *row_slots, *offsets, *counts;
+  uint32_t *workspace;
+};
+struct ExpertRows {
+  const void *x;  // gather: [tokens][cols]; combine: [rows][cols]; gradient: dout
+  const void *y;  // gradient: the rows that were combined
+  const int32_t *slot_rows, *row_slots;
+  const float *weights;
+  uint32_t tokens, topk, cols, rows;
+  void *out;
+  float *dweights;
+};
+uint64_t expert_sort_workspace_words(uint64_t slots, uint32_t experts);
+hipError_t launch_expert_sort(const ExpertSort &p, hipStream_t s);
+hipError_t launch_expert_gather(const ExpertRows &p, int dtype, hipStream_t s);
+hipError_t launch_expert_combine(const ExpertRows &p, int dtype, hipStream_t s);
+hipError_t launch_expert_combine_grad(const ExpertRows &p, int dtype, hipStream_t s);
+
+// Block-scaled FP8. pitch of a row of k elements: k rounded up to kFp8Block.
+constexpr uint32_t kFp8Block = 128;
+struct Fp8Quantize {
+  const void *x;  // [batch][rows][cols], or with row_slots [slots / topk][cols]
+  uint32_t batch, rows, cols;
+  const int32_t *row_slots;  // NULL: row r of x; else row row_slots[r] / topk (none: zeros)
+  uint32_t slots, topk;
+  uint8_t *row_data, *col_data;  // NULL: orientation not written
+  float *row_scales, *col_scales;
+};
+hipError_t launch_fp8_quantize(const Fp8Quantize &p, int dtype, bool block_2d, hipStream_t s);
+
+// d = a b^T by blocks of 128 along k; a always has 1x128 blocks.
+enum MatmulMode : uint32_t { kDense = 0, kGroupedRows = 1, kGroupedK = 2 };
+struct Fp8Matmul {
+  const uint8_t *a, *b;
+  const float *sa, *sb;
+  void *d;
+  uint32_t m, n, kblocks;  // rows of a (all groups'), rows of b (one group's), blocks of 128 along k (all groups')
+  uint32_t sa_stride, sb_stride;
+  bool b_block_2d, out_fp32;
+  uint32_t mode;
+  const int32_t *offsets;  // device, [groups + 1]
+  uint32_t groups;
+};
+hipError_t launch_fp8_matmul(const Fp8Matmul &p, hipStream_t s);
 hipError_t launch_debug_e2m1(const float *v, const uint32_t *r, uint8_t *out, uint64_t n, bool sr, bool pairwise,
                              hipStream_t s);
 hipError_t launch_debug_rht(const void *x, int dtype, uint32_t rows, uint32_t cols, uint32_t mask, float *t,
