@@ -14,7 +14,6 @@ Tensors passed in are torch CUDA tensors (on ROCm, HIP devices):
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import dataclasses
 import os
@@ -531,22 +530,23 @@ def _on(x: torch.Tensor, what: str) -> torch.device:
     return x.device
 
 
-def _as_stream(stream, device):
-    """The context that a call's outputs are allocated in, and the stream's handle."""
-    if stream is None:
-        return contextlib.nullcontext(), ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device)
-    return torch.cuda.stream(s), ctypes.c_void_p(s.cuda_stream)
+def _under(stream, device):
+    """The context of a call that was given a stream of its own."""
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device))
+
+
+def _current(device) -> int:
+    # the handle that torch.cuda.current_stream(device).cuda_stream has, without the object around it
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _want_plan(plan: ExpertPlan, device) -> None:
-    i32 = torch.int32
-    if plan.slot_rows.dim() != 2 or plan.row_slots.dim() != 1 or plan.counts.dim() != 1:
-        raise ValueError("a plan has slot_rows [tokens][topk], row_slots [rows] and counts [experts]")
-    _want(plan.slot_rows, i32, plan.slot_rows.shape, device, "plan.slot_rows")
-    _want(plan.row_slots, i32, plan.row_slots.shape, device, "plan.row_slots")
-    _want(plan.counts, i32, plan.counts.shape, device, "plan.counts")
-    _want(plan.offsets, i32, (plan.experts + 1,), device, "plan.offsets")
+    a, b, o, c, i32 = plan.slot_rows, plan.row_slots, plan.offsets, plan.counts, torch.int32
+    for t in (a, b, o, c):
+        if t.dtype != i32 or t.device != device or not t.is_contiguous():
+            raise ValueError(f"a plan's tensors must be contiguous int32 tensors on {device}, got {t.dtype} on {t.device}")
+    if a.dim() != 2 or b.dim() != 1 or c.dim() != 1 or o.dim() != 1 or o.shape[0] != c.shape[0] + 1:
+        raise ValueError("a plan has slot_rows [tokens][topk], row_slots [rows], offsets [experts + 1] and counts [experts]")
 
 
 def expert_sort(ids: torch.Tensor, experts: int, *, align: int = FP8_BLOCK, rows: Optional[int] = None,
@@ -562,16 +562,17 @@ def expert_sort(ids: torch.Tensor, experts: int, *, align: int = FP8_BLOCK, rows
     tokens, topk = ids.shape
     if rows is None:
         rows = int(lib.nvfp4_expert_rows(tokens, topk, experts, align))
-    ctx, s = _as_stream(stream, dev)
-    with ctx:
-        n = lib.nvfp4_expert_sort_workspace_bytes(tokens, topk, experts)
-        slot_rows = torch.empty((tokens, topk), dtype=torch.int32, device=dev)
-        row_slots = torch.empty((max(rows, 0),), dtype=torch.int32, device=dev)
-        offsets = torch.empty((max(experts, 0) + 1,), dtype=torch.int32, device=dev)
-        counts = torch.empty((max(experts, 0),), dtype=torch.int32, device=dev)
-        ws = torch.empty((n,), dtype=torch.uint8, device=dev) if n else None
-        _check(lib.nvfp4_expert_sort(_ptr(ids), ids.element_size(), tokens, topk, experts, align, rows, _ptr(slot_rows),
-                                     _ptr(row_slots), _ptr(offsets), _ptr(counts), _ptr(ws), s))
+    if stream is not None:
+        with _under(stream, dev):
+            return expert_sort(ids, experts, align=align, rows=rows)
+    n = lib.nvfp4_expert_sort_workspace_bytes(tokens, topk, experts)
+    slot_rows = torch.empty((tokens, topk), dtype=torch.int32, device=dev)
+    row_slots = torch.empty((max(rows, 0),), dtype=torch.int32, device=dev)
+    offsets = torch.empty((max(experts, 0) + 1,), dtype=torch.int32, device=dev)
+    counts = torch.empty((max(experts, 0),), dtype=torch.int32, device=dev)
+    ws = torch.empty((n,), dtype=torch.uint8, device=dev) if n else None
+    _check(lib.nvfp4_expert_sort(_ptr(ids), ids.element_size(), tokens, topk, experts, align, rows, _ptr(slot_rows),
+                                 _ptr(row_slots), _ptr(offsets), _ptr(counts), _ptr(ws), _current(dev)))
     return ExpertPlan(slot_rows, row_slots, offsets, counts, align)
 
 
@@ -582,11 +583,12 @@ def expert_gather(x: torch.Tensor, plan: ExpertPlan, *, stream=None) -> torch.Te
     if x.dim() != 2 or x.shape[0] != plan.tokens:
         raise ValueError(f"x must be [{plan.tokens}][cols], got {tuple(x.shape)}")
     code = _dtype_code(x)
-    ctx, s = _as_stream(stream, dev)
-    with ctx:
-        y = torch.empty((plan.rows, x.shape[1]), dtype=x.dtype, device=dev)
-        _check(load().nvfp4_expert_gather(_ptr(x), code, plan.tokens, plan.topk, x.shape[1], _ptr(plan.row_slots), plan.rows,
-                                          _ptr(y), s))
+    if stream is not None:
+        with _under(stream, dev):
+            return expert_gather(x, plan)
+    y = torch.empty((plan.rows, x.shape[1]), dtype=x.dtype, device=dev)
+    _check(load().nvfp4_expert_gather(_ptr(x), code, plan.tokens, plan.topk, x.shape[1], _ptr(plan.row_slots), plan.rows,
+                                      _ptr(y), _current(dev)))
     return y
 
 
@@ -601,11 +603,12 @@ def expert_combine(y: torch.Tensor, plan: ExpertPlan, weights: Optional[torch.Te
     if weights is not None:
         _want(weights, torch.float32, (plan.tokens, plan.topk), dev, "weights")
     code = _dtype_code(y)
-    ctx, s = _as_stream(stream, dev)
-    with ctx:
-        out = torch.empty((plan.tokens, y.shape[1]), dtype=y.dtype, device=dev)
-        _check(load().nvfp4_expert_combine(_ptr(y), code, plan.tokens, plan.topk, y.shape[1], _ptr(plan.slot_rows), plan.rows,
-                                           _ptr(weights), _ptr(out), s))
+    if stream is not None:
+        with _under(stream, dev):
+            return expert_combine(y, plan, weights)
+    out = torch.empty((plan.tokens, y.shape[1]), dtype=y.dtype, device=dev)
+    _check(load().nvfp4_expert_combine(_ptr(y), code, plan.tokens, plan.topk, y.shape[1], _ptr(plan.slot_rows), plan.rows,
+                                       _ptr(weights), _ptr(out), _current(dev)))
     return out
 
 
@@ -625,12 +628,13 @@ def expert_combine_grad(dout: torch.Tensor, y: torch.Tensor, plan: ExpertPlan, w
     _want(y, dout.dtype, (plan.rows, cols), dev, "y")
     _want(weights, torch.float32, (plan.tokens, plan.topk), dev, "weights")
     code = _dtype_code(dout)
-    ctx, s = _as_stream(stream, dev)
-    with ctx:
-        dy = torch.empty((plan.rows, cols), dtype=dout.dtype, device=dev)
-        dw = torch.empty((plan.tokens, plan.topk), dtype=torch.float32, device=dev)
-        _check(load().nvfp4_expert_combine_grad(_ptr(dout), _ptr(y), code, plan.tokens, plan.topk, cols, _ptr(plan.slot_rows),
-                                                _ptr(plan.row_slots), plan.rows, _ptr(weights), _ptr(dy), _ptr(dw), s))
+    if stream is not None:
+        with _under(stream, dev):
+            return expert_combine_grad(dout, y, plan, weights)
+    dy = torch.empty((plan.rows, cols), dtype=dout.dtype, device=dev)
+    dw = torch.empty((plan.tokens, plan.topk), dtype=torch.float32, device=dev)
+    _check(load().nvfp4_expert_combine_grad(_ptr(dout), _ptr(y), code, plan.tokens, plan.topk, cols, _ptr(plan.slot_rows),
+                                            _ptr(plan.row_slots), plan.rows, _ptr(weights), _ptr(dy), _ptr(dw), _current(dev)))
     return dy, dw
 
 
@@ -660,18 +664,19 @@ def fp8_quantize(x: torch.Tensor, *, rowwise=True, columnwise=False, block_2d=Fa
         if rows != plan.tokens:
             raise ValueError(f"x must be [{plan.tokens}][cols], got {tuple(x.shape)}")
         slots, tokens, topk, rows = plan.row_slots, plan.tokens, plan.topk, plan.rows
-    ctx, s = _as_stream(stream, dev)
+    if stream is not None:
+        with _under(stream, dev):
+            return fp8_quantize(x, rowwise=rowwise, columnwise=columnwise, block_2d=block_2d, plan=plan)
 
     def empty(n, k):
         return Fp8Tensor(torch.empty((*lead, n, _blocks(k) * FP8_BLOCK), dtype=torch.float8_e4m3fn, device=dev),
                          torch.empty((*lead, _blocks(k), _blocks(n) if block_2d else n), dtype=torch.float32, device=dev),
                          n, k, bool(block_2d))
 
-    with ctx:
-        row = empty(rows, cols) if rowwise else None
-        col = empty(cols, rows) if columnwise else None
-        r, c = row.as_c() if row is not None else None, col.as_c() if col is not None else None
-        _check(load().nvfp4_fp8_quantize(_ptr(x), code, batch, rows, cols, _ptr(slots), tokens, topk, int(block_2d), r, c, s))
+    row = empty(rows, cols) if rowwise else None
+    col = empty(cols, rows) if columnwise else None
+    r, c = row.as_c() if row is not None else None, col.as_c() if col is not None else None
+    _check(load().nvfp4_fp8_quantize(_ptr(x), code, batch, rows, cols, _ptr(slots), tokens, topk, int(block_2d), r, c, _current(dev)))
     return row, col
 
 
@@ -696,10 +701,11 @@ def fp8_matmul(a: Fp8Tensor, b: Fp8Tensor, *, out_dtype=torch.bfloat16, stream=N
     code = _out_code(out_dtype)
     _want_fp8(a, (), a.n, a.k, False, dev, "operand a")
     _want_fp8(b, (), b.n, a.k, bool(b.block_2d), dev, "operand b")
-    ctx, s = _as_stream(stream, dev)
-    with ctx:
-        d = torch.empty((a.n, b.n), dtype=out_dtype, device=dev)
-        _check(load().nvfp4_fp8_matmul(a.as_c(), b.as_c(), a.n, b.n, a.k, int(b.block_2d), _ptr(d), code, s))
+    if stream is not None:
+        with _under(stream, dev):
+            return fp8_matmul(a, b, out_dtype=out_dtype)
+    d = torch.empty((a.n, b.n), dtype=out_dtype, device=dev)
+    _check(load().nvfp4_fp8_matmul(a.as_c(), b.as_c(), a.n, b.n, a.k, int(b.block_2d), _ptr(d), code, _current(dev)))
     return d
 
 
@@ -712,11 +718,12 @@ def fp8_matmul_grouped(a: Fp8Tensor, b: Fp8Tensor, plan: ExpertPlan, *, out_dtyp
     _want_plan(plan, dev)
     _want_fp8(a, (), plan.rows, a.k, False, dev, "operand a")
     _want_fp8(b, (plan.experts,), b.n, a.k, True, dev, "operand b")
-    ctx, s = _as_stream(stream, dev)
-    with ctx:
-        d = torch.empty((plan.rows, b.n), dtype=out_dtype, device=dev)
-        _check(load().nvfp4_fp8_matmul_grouped(a.as_c(), b.as_c(), _ptr(plan.offsets), plan.experts, plan.rows, b.n, a.k,
-                                               _ptr(d), code, s))
+    if stream is not None:
+        with _under(stream, dev):
+            return fp8_matmul_grouped(a, b, plan, out_dtype=out_dtype)
+    d = torch.empty((plan.rows, b.n), dtype=out_dtype, device=dev)
+    _check(load().nvfp4_fp8_matmul_grouped(a.as_c(), b.as_c(), _ptr(plan.offsets), plan.experts, plan.rows, b.n, a.k,
+                                           _ptr(d), code, _current(dev)))
     return d
 
 
@@ -731,9 +738,10 @@ def fp8_matmul_grouped_k(a: Fp8Tensor, b: Fp8Tensor, plan: ExpertPlan, *, out_dt
         raise ValueError(f"the plan must be aligned to {FP8_BLOCK} rows, got {plan.align}")
     _want_fp8(a, (), a.n, plan.rows, False, dev, "operand a")
     _want_fp8(b, (), b.n, plan.rows, False, dev, "operand b")
-    ctx, s = _as_stream(stream, dev)
-    with ctx:
-        d = torch.empty((plan.experts, a.n, b.n), dtype=out_dtype, device=dev)
-        _check(load().nvfp4_fp8_matmul_grouped_k(a.as_c(), b.as_c(), _ptr(plan.offsets), plan.experts, a.n, b.n, plan.rows,
-                                                 _ptr(d), code, s))
+    if stream is not None:
+        with _under(stream, dev):
+            return fp8_matmul_grouped_k(a, b, plan, out_dtype=out_dtype)
+    d = torch.empty((plan.experts, a.n, b.n), dtype=out_dtype, device=dev)
+    _check(load().nvfp4_fp8_matmul_grouped_k(a.as_c(), b.as_c(), _ptr(plan.offsets), plan.experts, a.n, b.n, plan.rows,
+                                             _ptr(d), code, _current(dev)))
     return d

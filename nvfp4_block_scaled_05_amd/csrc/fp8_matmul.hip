@@ -100,18 +100,35 @@ __device__ __forceinline__ Part find_rows(const Args &p, uint32_t tile) {
   return r;
 }
 
+// Workgroup `id`'s tile. Workgroups go to the eight XCDs in turn, each of
+// which has an L2 of its own: so each XCD gets runs of 32 consecutive places,
+// and places run through patches of kPatch tile rows, column by column, so
+// that the 32 tiles that an XCD works on at a time share their operands.
+constexpr uint32_t kXcds = 8, kRun = 32, kPatch = 4;
+__device__ __forceinline__ void tile_of(uint32_t id, const Args &p, uint32_t &tm, uint32_t &tn) {
+  const uint32_t total = gridDim.x;
+  if (id < total / (kXcds * kRun) * (kXcds * kRun)) {
+    const uint32_t in = id % (kXcds * kRun);
+    id = id - in + in % kXcds * kRun + in / kXcds;
+  }
+  const uint32_t rows = total / p.tiles_n, band = id / (kPatch * p.tiles_n), in = id - band * kPatch * p.tiles_n;
+  const uint32_t high = min(kPatch, rows - band * kPatch);
+  tm = band * kPatch + in % high;
+  tn = in / high;
+}
+
 template <bool OUT32>
 __device__ __forceinline__ void store1(void *d, uint64_t at, float v) {
   if (OUT32) static_cast<float *>(d)[at] = v;
   else static_cast<uint16_t *>(d)[at] = static_cast<uint16_t>(bf16_pair(v, 0.0f));
 }
 
-// Values v[0 .. 15] to columns j .. j + 15 of a row of d that starts at `row`.
-template <bool OUT32>
-__device__ __forceinline__ void store16(void *d, uint64_t row, uint32_t j, uint32_t n, const float *v) {
+// Values v[0 .. N - 1] to columns j .. j + N - 1 of a row of d that starts at `row`.
+template <bool OUT32, uint32_t N>
+__device__ __forceinline__ void store(void *d, uint64_t row, uint32_t j, uint32_t n, const float *v) {
   constexpr uint32_t per = OUT32 ? 4 : 8;
 #pragma unroll
-  for (uint32_t i = 0; i < 16; i += per) {
+  for (uint32_t i = 0; i < N; i += per) {
     if (j + i + per <= n) {
       u32x4_any w;
 #pragma unroll
@@ -129,7 +146,7 @@ __device__ __forceinline__ void store16(void *d, uint64_t row, uint32_t j, uint3
 // Loads straight to LDS, 16 bytes or 4 a lane: lane l's go to `to` + 16 l (4 l),
 // from `from` + `offset`. Written out, since the compiler waits for every
 // such load before the next LDS read, whichever stage it reads. They have no
-// destination register; wait_loads() waits for all of them.
+// destination register; wait_loads() waits until at most LEFT are on their way.
 __device__ __forceinline__ uint32_t lds_address(const void *p) {
   return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const void *)p));
 }
@@ -144,7 +161,10 @@ __device__ __forceinline__ void load4_to_lds(uint32_t to, const void *from, uint
   asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %2, %3\n\ts_mov_b32 m0, %0"
                : "=&s"(keep) : "s"(to), "v"(offset), "s"(from) : "memory");
 }
-__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+template <uint32_t LEFT>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LEFT) : "memory");
+}
 
 // 16 codes to BF16: the eight of the first two words and of the last two.
 struct Wide {
@@ -160,8 +180,16 @@ __device__ __forceinline__ Wide widen(u32x4 w) { return Wide{widen8(w.x, w.y), w
 
 // ---------------------------------------------------------------------------
 // Tiles of BM x BN, WM x WN waves, each wave (BM / WM) x (BN / WN). A step
-// along k is one block of 128 bytes of every row; two stages in LDS, the next
-// one filled by loads straight to LDS while the matrix cores work on this one.
+// along k is one block of 128 bytes of every row; ST stages in LDS, filled by
+// loads straight to LDS while the matrix cores work on the oldest one.
+//
+// At 8192 x 8192 x 5120 this takes 570 us (1.2 PFLOP/s) in 128x128 tiles, two
+// workgroups a CU. The widening and the scaling are 3 vector instructions
+// for each v_mfma; measured alone, a v_mfma takes 17 cycles with up to two
+// of them beside it and 22 with three, and the mix of this kernel from
+// registers only 25, against 29 here. The rest is power: the clock drops to
+// 2.1 GHz. 32x32x16 v_mfma, which leave more room beside them, need 5% fewer
+// cycles and take 590 us, at 1.9 GHz.
 //
 // LDS layout: rows of 128 bytes, eight 16-byte chunks, chunk g of row r at
 // place g ^ f(r), so that lanes that read one chunk of neighbouring rows meet
@@ -169,21 +197,29 @@ __device__ __forceinline__ Wide widen(u32x4 w) { return Wide{widen8(w.x, w.y), w
 // is in the addresses that they read from.
 // The matrix core's first operand is b, its second a: lane l then holds, for
 // row l % 16 of a, four consecutive rows 4 (l / 16) .. of the 16x16 tile's
-// b. Which rows of b a tile takes is free: tile i of four takes rows
-// 16 q + 4 i + r of a group of 64 as its rows 4 q + r, so that a lane ends
-// with 16 consecutive columns of d and stores 16 bytes at a time.
+// b. Which rows of b a tile takes is free: tile j of G takes rows 4 G q + 4 j
+// + r of a group of 16 G as its rows 4 q + r, so that a lane ends with 4 G
+// consecutive columns of d and stores 16 bytes at a time.
 // ---------------------------------------------------------------------------
-template <uint32_t BM, uint32_t BN, uint32_t WM, uint32_t WN, bool SBV, bool OUT32>
+// f(r) of b: with that order of its rows, eight lanes that follow each other get eight values
+template <uint32_t G>
+__device__ __forceinline__ uint32_t swizzle_b(uint32_t r) { return (r & 3) | (r / (4 * G) & 1) << 2; }
+
+template <uint32_t BM, uint32_t BN, uint32_t WM, uint32_t WN, uint32_t ST, bool SBV, bool OUT32>
 __global__ __launch_bounds__(WM *WN *kWave) void k_fp8_tile(Args p) {
   constexpr uint32_t kWaves = WM * WN;
-  constexpr uint32_t TM = BM / WM, TN = BN / WN, MI = TM / 16, NI = TN / 16, NG = TN / 64;
+  constexpr uint32_t TM = BM / WM, TN = BN / WN, MI = TM / 16, NI = TN / 16;
+  constexpr uint32_t G = NI < 4 ? NI : 4, NG = NI / G;  // 16-row tiles of b that share 16 G rows
   constexpr uint32_t kLoadA = BM / 8 / kWaves, kLoadB = BN / 8 / kWaves;  // loads of 8 rows that a wave makes
-  static_assert(TN % 64 == 0 && BM % (8 * kWaves) == 0 && BN % (8 * kWaves) == 0 && (BM + BN) / 64 <= kWaves, "tile shape");
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2][(BM + BN) * kBlock];
-  __shared__ __attribute__((aligned(16))) float scales[2][BM + BN];
+  constexpr uint32_t kGroups = (BM + BN) / 64, kLoadS = (kGroups + kWaves - 1) / kWaves, kLoads = kLoadA + kLoadB + kLoadS;
+  static_assert((NI == 2 || NI % 4 == 0) && BM % (8 * kWaves) == 0 && BN % (8 * kWaves) == 0, "tile shape");
+  static_assert((ST - 2) * kLoads < 64, "loads in flight");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[ST][(BM + BN) * kBlock];
+  __shared__ __attribute__((aligned(16))) float scales[ST][BM + BN];
 
   const uint32_t lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  uint32_t tn = blockIdx.x % p.tiles_n, tm = blockIdx.x / p.tiles_n;
+  uint32_t tm, tn;
+  tile_of(blockIdx.x, p, tm, tn);
   Part part{tm * BM, p.m, 0, p.kblocks, 0, false};
   uint64_t d_base = 0;
   if (p.mode == kGroupedRows) {
@@ -217,15 +253,17 @@ __global__ __launch_bounds__(WM *WN *kWave) void k_fp8_tile(Args p) {
 #pragma unroll
   for (uint32_t i = 0; i < kLoadB; ++i) {
     const uint32_t r = (wave * kLoadB + i) * 8 + lane / 8;
-    from_b[i] = min(r, p.n - 1 - n0) * static_cast<uint32_t>(pitch) + ((chunk ^ ((r & 3) | ((r >> 2) & 4))) << 4);
+    from_b[i] = min(r, p.n - 1 - n0) * static_cast<uint32_t>(pitch) + ((chunk ^ swizzle_b<G>(r)) << 4);
   }
   if (SBV) sb += n0;
-  // scales: a wave's 64 are those of 64 rows of a, or of b; of b in 128x128 blocks, 64 times its block's
-  const bool scale_of_b = wave >= BM / 64;
-  const uint32_t s_row = (wave - (scale_of_b ? BM / 64 : 0)) * 64 + lane;
-  const uint32_t from_s = !scale_of_b ? min(s_row, part.m_end - 1 - m0)
-                          : SBV       ? min(s_row, p.n - 1 - n0)
-                                      : min((n0 + s_row) / kBlock, p.sb_stride - 1);
+  // scales: 64 at a time, of 64 rows of a or of b; of b in 128x128 blocks, 64 times its block's.
+  // Every wave makes as many loads, some of them twice, so that each can count its own.
+  uint32_t from_s[kLoadS];
+#pragma unroll
+  for (uint32_t i = 0; i < kLoadS; ++i) {
+    const uint32_t w = (wave * kLoadS + i) % kGroups, r = (w < BM / 64 ? w : w - BM / 64) * 64 + lane;
+    from_s[i] = 4 * (w < BM / 64 ? min(r, part.m_end - 1 - m0) : SBV ? min(r, p.n - 1 - n0) : min((n0 + r) / kBlock, p.sb_stride - 1));
+  }
 
   const uint32_t lds_data = lds_address(&lds[0][0]), lds_scales = lds_address(&scales[0][0]);
   auto load = [&](uint32_t kb, uint32_t stage) {
@@ -235,9 +273,12 @@ __global__ __launch_bounds__(WM *WN *kWave) void k_fp8_tile(Args p) {
     for (uint32_t i = 0; i < kLoadA; ++i) load16_to_lds(to + (wave * kLoadA + i) * 1024, ka, from_a[i]);
 #pragma unroll
     for (uint32_t i = 0; i < kLoadB; ++i) load16_to_lds(to + BM * kBlock + (wave * kLoadB + i) * 1024, kbp, from_b[i]);
-    const uint32_t to_s = lds_scales + stage * static_cast<uint32_t>(sizeof scales[0]) + wave * 256;
-    if (!scale_of_b) load4_to_lds(to_s, sa + static_cast<uint64_t>(kb) * p.sa_stride, 4 * from_s);
-    else if (wave < (BM + BN) / 64) load4_to_lds(to_s, sb + static_cast<uint64_t>(kb) * p.sb_stride, 4 * from_s);
+#pragma unroll
+    for (uint32_t i = 0; i < kLoadS; ++i) {
+      const uint32_t w = (wave * kLoadS + i) % kGroups;
+      load4_to_lds(lds_scales + stage * static_cast<uint32_t>(sizeof scales[0]) + w * 256,
+                   w < BM / 64 ? sa + static_cast<uint64_t>(kb) * p.sa_stride : sb + static_cast<uint64_t>(kb) * p.sb_stride, from_s[i]);
+    }
   };
 
   const uint32_t wm = wave % WM, wn = wave / WM;
@@ -254,23 +295,23 @@ __global__ __launch_bounds__(WM *WN *kWave) void k_fp8_tile(Args p) {
     return *reinterpret_cast<const u32x4 *>(base + r * kBlock + ((g ^ f) << 4));
   };
 
-  auto step = [&](uint32_t kb, uint32_t stage) {
+  auto step = [&](uint32_t stage) {
     const uint8_t *la = &lds[stage][wm * TM * kBlock], *lb = &lds[stage][(BM + wn * TN) * kBlock];
     const float *ls = &scales[stage][wm * TM], *lsb = &scales[stage][BM + wn * TN];
     float sbu[NG];
     if (!SBV) {
 #pragma unroll
-      for (uint32_t g = 0; g < NG; ++g) sbu[g] = lsb[64 * g];
+      for (uint32_t g = 0; g < NG; ++g) sbu[g] = lsb[16 * G * g];
     }
     Wide b0[NI], b1[NI];
     f32x4 sbv[NI];
 #pragma unroll
     for (uint32_t j = 0; j < NI; ++j) {
-      const uint32_t r = (j / 4) * 64 + (i16 / 4) * 16 + (j % 4) * 4 + i16 % 4;
-      const uint32_t f = i16 & 7;  // f(r): r's low two bits and its bit 4
+      const uint32_t r = (j / G) * 16 * G + (i16 / 4) * 4 * G + (j % G) * 4 + i16 % 4;
+      const uint32_t f = i16 & 7;  // f(r): r's low two bits and the lowest bit of i16 / 4
       b0[j] = widen(chunk_at(lb, r, q, f));
       b1[j] = widen(chunk_at(lb, r, q + 4, f));
-      if (SBV) sbv[j] = *reinterpret_cast<const f32x4 *>(lsb + (j / 4) * 64 + q * 16 + (j % 4) * 4);
+      if (SBV) sbv[j] = *reinterpret_cast<const f32x4 *>(lsb + (j / G) * 16 * G + q * 4 * G + (j % G) * 4);
     }
 #pragma unroll
     for (uint32_t i = 0; i < MI; ++i) {
@@ -283,20 +324,24 @@ __global__ __launch_bounds__(WM *WN *kWave) void k_fp8_tile(Args p) {
         c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b1[j].lo, a1.lo, c, 0, 0, 0);
         c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b1[j].hi, a1.hi, c, 0, 0, 0);
 #pragma unroll
-        for (uint32_t e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(c[e], SBV ? s * sbv[j][e] : s * sbu[j / 4], acc[i][j][e]);
+        for (uint32_t e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(c[e], SBV ? s * sbv[j][e] : s * sbu[j / G], acc[i][j][e]);
       }
     }
   };
 
   if (!part.zero && part.kb0 < part.kb_end) {
-    load(part.kb0, 0);
+#pragma unroll
+    for (uint32_t i = 0; i + 1 < ST; ++i) load(min(part.kb0 + i, part.kb_end - 1), i);
+    uint32_t stage = 0;
     for (uint32_t kb = part.kb0; kb < part.kb_end; ++kb) {
-      const uint32_t stage = (kb - part.kb0) & 1;
-      wait_loads();   // this step's loads are in,
-      lds_barrier();  // everyone's are, and everyone has read the other stage
-      if (kb + 1 < part.kb_end) load(kb + 1, stage ^ 1);
-      step(kb, stage);
+      wait_loads<(ST - 2) * kLoads>();  // this step's loads are in,
+      lds_barrier();                    // everyone's are, and everyone has read the stage that is filled next
+      // past the end the last block comes again, so that the loads in flight stay as many
+      if (ST > 2 || kb + 1 < part.kb_end) load(min(kb + ST - 1, part.kb_end - 1), stage == 0 ? ST - 1 : stage - 1);
+      step(stage);
+      stage = stage + 1 == ST ? 0 : stage + 1;
     }
+    if (ST > 2) wait_loads<0>();  // nothing writes to LDS after the end
   }
 
 #pragma unroll
@@ -306,15 +351,174 @@ __global__ __launch_bounds__(WM *WN *kWave) void k_fp8_tile(Args p) {
     const uint64_t row = d_base + static_cast<uint64_t>(m) * p.n;
 #pragma unroll
     for (uint32_t g = 0; g < NG; ++g) {
-      float v[16];
+      float v[4 * G];
 #pragma unroll
-      for (uint32_t e = 0; e < 16; ++e) v[e] = acc[i][4 * g + e / 4][e % 4];
-      store16<OUT32>(p.d, row, n0 + wn * TN + 64 * g + 16 * q, p.n, v);
+      for (uint32_t e = 0; e < 4 * G; ++e) v[e] = acc[i][G * g + e / 4][e % 4];
+      store<OUT32, 4 * G>(p.d, row, n0 + wn * TN + 16 * G * g + 4 * G * q, p.n, v);
     }
   }
 }
 
-template <uint32_t BM, uint32_t BN, uint32_t WM, uint32_t WN>
+// ---------------------------------------------------------------------------
+// Few rows: tiles of up to kRowsM rows and kRowsN columns, the blocks along k
+// dealt out to the KS waves of a workgroup, each with accumulators of its own,
+// which meet in LDS at the end, in the order of the waves. Operands go from
+// memory to registers, U blocks of them asked for before the first is used:
+// each row of b is read once and by one wave, so LDS would only add a step.
+// ---------------------------------------------------------------------------
+constexpr uint32_t kRowsM = 64, kRowsN = 32;
+
+template <bool OUT32>
+__device__ __forceinline__ void store4(void *d, uint64_t row, uint32_t j, uint32_t n, f32x4 v) {
+  if (j + 4 <= n) {
+    if (OUT32) {
+      *reinterpret_cast<u32x4_any *>(static_cast<float *>(d) + row + j) =
+          u32x4_any{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+    } else {
+      typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
+      *reinterpret_cast<u32x2_any *>(static_cast<uint16_t *>(d) + row + j) = u32x2_any{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+    }
+  } else {
+#pragma unroll
+    for (uint32_t q = 0; q < 4; ++q)
+      if (j + q < n) store1<OUT32>(d, row + j + q, v[q]);
+  }
+}
+
+template <uint32_t KS, uint32_t MT, uint32_t U, bool SBV, bool OUT32>
+__device__ __forceinline__ void rows_tile(const Args &p, const Part &part, const uint8_t *a, const uint8_t *b, const float *sa,
+                                          const float *sb, uint32_t n0, f32x4 (*red)[kRowsM / 16 * 2][kWave]) {
+  const uint32_t lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const uint32_t i16 = lane % 16, q = lane / 16;
+  const uint32_t pitch = p.kblocks * kBlock;
+  // tile t of b takes rows 8 (i / 4) + 4 t + i % 4, so that a lane ends with 8 consecutive columns of d
+  uint32_t at_a[MT], at_b[2], row_a[MT];
+#pragma unroll
+  for (uint32_t i = 0; i < MT; ++i) {
+    row_a[i] = min(16 * i + i16, part.m_end - 1 - part.m0);
+    at_a[i] = row_a[i] * pitch + 16 * q;
+  }
+#pragma unroll
+  for (uint32_t t = 0; t < 2; ++t) at_b[t] = min(8 * (i16 / 4) + 4 * t + i16 % 4, p.n - 1 - n0) * pitch + 16 * q;
+  uint32_t row_sb[2][4];
+  if (SBV) {
+#pragma unroll
+    for (uint32_t t = 0; t < 2; ++t)
+#pragma unroll
+      for (uint32_t e = 0; e < 4; ++e) row_sb[t][e] = min(8 * q + 4 * t + e, p.n - 1 - n0);
+  }
+  const uint32_t nb = n0 / kBlock;
+
+  f32x4 acc[MT][2];
+#pragma unroll
+  for (uint32_t i = 0; i < MT; ++i) acc[i][0] = acc[i][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (uint32_t kb0 = part.kb0 + wave; kb0 < part.kb_end; kb0 += U * KS) {
+    u32x4 wa[U][MT][2], wb[U][2][2];
+    float fa[U][MT], fb[U][2][4];
+#pragma unroll
+    for (uint32_t u = 0; u < U; ++u) {
+      const uint32_t kb = min(kb0 + u * KS, part.kb_end - 1);  // past the end: loaded again, not used
+      const uint8_t *ka = a + static_cast<uint64_t>(kb) * kBlock, *kbp = b + static_cast<uint64_t>(kb) * kBlock;
+#pragma unroll
+      for (uint32_t t = 0; t < 2; ++t) {
+        wb[u][t][0] = *reinterpret_cast<const u32x4 *>(kbp + at_b[t]);
+        wb[u][t][1] = *reinterpret_cast<const u32x4 *>(kbp + at_b[t] + 64);
+      }
+#pragma unroll
+      for (uint32_t i = 0; i < MT; ++i) {
+        wa[u][i][0] = *reinterpret_cast<const u32x4 *>(ka + at_a[i]);
+        wa[u][i][1] = *reinterpret_cast<const u32x4 *>(ka + at_a[i] + 64);
+        fa[u][i] = sa[static_cast<uint64_t>(kb) * p.sa_stride + row_a[i]];
+      }
+      if (SBV) {
+#pragma unroll
+        for (uint32_t t = 0; t < 2; ++t)
+#pragma unroll
+          for (uint32_t e = 0; e < 4; ++e) fb[u][t][e] = sb[static_cast<uint64_t>(kb) * p.sb_stride + n0 + row_sb[t][e]];
+      } else {
+        fb[u][0][0] = sb[static_cast<uint64_t>(kb) * p.sb_stride + nb];
+      }
+    }
+#pragma unroll
+    for (uint32_t u = 0; u < U; ++u) {
+      if (kb0 + u * KS >= part.kb_end) break;
+      Wide b0[2], b1[2];
+#pragma unroll
+      for (uint32_t t = 0; t < 2; ++t) {
+        b0[t] = widen(wb[u][t][0]);
+        b1[t] = widen(wb[u][t][1]);
+      }
+#pragma unroll
+      for (uint32_t i = 0; i < MT; ++i) {
+        const Wide a0 = widen(wa[u][i][0]), a1 = widen(wa[u][i][1]);
+#pragma unroll
+        for (uint32_t t = 0; t < 2; ++t) {
+          f32x4 c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b0[t].lo, a0.lo, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
+          c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b0[t].hi, a0.hi, c, 0, 0, 0);
+          c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b1[t].lo, a1.lo, c, 0, 0, 0);
+          c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b1[t].hi, a1.hi, c, 0, 0, 0);
+#pragma unroll
+          for (uint32_t e = 0; e < 4; ++e) acc[i][t][e] = __builtin_fmaf(c[e], fa[u][i] * fb[u][SBV ? t : 0][SBV ? e : 0], acc[i][t][e]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (uint32_t i = 0; i < MT; ++i)
+#pragma unroll
+    for (uint32_t t = 0; t < 2; ++t) red[wave][2 * i + t][lane] = acc[i][t];
+  lds_barrier();
+  for (uint32_t it = wave; it < 2 * MT; it += KS) {
+    f32x4 v = red[0][it][lane];
+#pragma unroll
+    for (uint32_t w = 1; w < KS; ++w) v += red[w][it][lane];
+    const uint32_t m = part.m0 + 16 * (it / 2) + i16;
+    if (m < part.m_end) store4<OUT32>(p.d, static_cast<uint64_t>(m) * p.n, n0 + 8 * q + 4 * (it % 2), p.n, v);
+  }
+}
+
+template <uint32_t KS, bool SBV, bool OUT32>
+__global__ __launch_bounds__(KS *kWave) void k_fp8_rows(Args p) {
+  __shared__ f32x4 red[KS][kRowsM / 16 * 2][kWave];
+  const uint32_t tn = blockIdx.x % p.tiles_n, tm = blockIdx.x / p.tiles_n;
+  Part part{tm * kRowsM, min(p.m, (tm + 1) * kRowsM), 0, p.kblocks, 0, false};
+  if (p.mode == kGroupedRows) {
+    part = find_rows<kRowsM>(p, tm);
+    if (part.m0 >= part.m_end) return;
+    part.m_end = min(part.m_end, part.m0 + kRowsM);
+    if (part.zero) part.kb_end = 0;
+  }
+  const uint32_t n0 = tn * kRowsN;
+  const uint64_t pitch = static_cast<uint64_t>(p.kblocks) * kBlock;
+  const uint8_t *a = p.a + part.m0 * pitch, *b = p.b + n0 * pitch;
+  const float *sa = p.sa + part.m0, *sb = p.sb;
+  if (p.mode == kGroupedRows) {
+    b += static_cast<uint64_t>(part.group) * p.n * pitch;
+    sb += static_cast<uint64_t>(part.group) * p.sb_stride * p.kblocks;
+  }
+  const uint32_t rows = part.m_end - part.m0;
+  if (rows <= 16) rows_tile<KS, 1, 4, SBV, OUT32>(p, part, a, b, sa, sb, n0, red);
+  else if (rows <= 32) rows_tile<KS, 2, 2, SBV, OUT32>(p, part, a, b, sa, sb, n0, red);
+  else rows_tile<KS, 4, 2, SBV, OUT32>(p, part, a, b, sa, sb, n0, red);
+}
+
+template <uint32_t KS>
+hipError_t launch_rows(const Fp8Matmul &p, hipStream_t s) {
+  Args a{p.a, p.b, p.sa, p.sb, p.d, p.m, p.n, p.kblocks, p.sa_stride, p.sb_stride, p.mode, p.offsets, p.groups, 0, 0};
+  a.tiles_n = (p.n + kRowsN - 1) / kRowsN;
+  a.tiles_m = p.mode == kGroupedRows ? p.m / kRowsM + p.groups + 1 : (p.m + kRowsM - 1) / kRowsM;
+  const dim3 grid(a.tiles_m * a.tiles_n), threads(KS * kWave);
+  if (p.b_block_2d) {
+    if (p.out_fp32) hipLaunchKernelGGL((k_fp8_rows<KS, false, true>), grid, threads, 0, s, a);
+    else hipLaunchKernelGGL((k_fp8_rows<KS, false, false>), grid, threads, 0, s, a);
+  } else {
+    if (p.out_fp32) hipLaunchKernelGGL((k_fp8_rows<KS, true, true>), grid, threads, 0, s, a);
+    else hipLaunchKernelGGL((k_fp8_rows<KS, true, false>), grid, threads, 0, s, a);
+  }
+  return hipGetLastError();
+}
+
+template <uint32_t BM, uint32_t BN, uint32_t WM, uint32_t WN, uint32_t ST>
 hipError_t launch_tile(const Fp8Matmul &p, hipStream_t s) {
   Args a{p.a, p.b, p.sa, p.sb, p.d, p.m, p.n, p.kblocks, p.sa_stride, p.sb_stride, p.mode, p.offsets, p.groups, 0, 0};
   a.tiles_n = (p.n + BN - 1) / BN;
@@ -327,17 +531,39 @@ hipError_t launch_tile(const Fp8Matmul &p, hipStream_t s) {
   if (blocks >= (uint64_t{1} << 31)) return hipErrorInvalidConfiguration;
   const dim3 grid(static_cast<uint32_t>(blocks)), threads(WM * WN * kWave);
   if (p.b_block_2d) {
-    if (p.out_fp32) hipLaunchKernelGGL((k_fp8_tile<BM, BN, WM, WN, false, true>), grid, threads, 0, s, a);
-    else hipLaunchKernelGGL((k_fp8_tile<BM, BN, WM, WN, false, false>), grid, threads, 0, s, a);
+    if (p.out_fp32) hipLaunchKernelGGL((k_fp8_tile<BM, BN, WM, WN, ST, false, true>), grid, threads, 0, s, a);
+    else hipLaunchKernelGGL((k_fp8_tile<BM, BN, WM, WN, ST, false, false>), grid, threads, 0, s, a);
   } else {
-    if (p.out_fp32) hipLaunchKernelGGL((k_fp8_tile<BM, BN, WM, WN, true, true>), grid, threads, 0, s, a);
-    else hipLaunchKernelGGL((k_fp8_tile<BM, BN, WM, WN, true, false>), grid, threads, 0, s, a);
+    if (p.out_fp32) hipLaunchKernelGGL((k_fp8_tile<BM, BN, WM, WN, ST, true, true>), grid, threads, 0, s, a);
+    else hipLaunchKernelGGL((k_fp8_tile<BM, BN, WM, WN, ST, true, false>), grid, threads, 0, s, a);
   }
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_fp8_matmul(const Fp8Matmul &p, hipStream_t s) { return launch_tile<128, 128, 2, 2>(p, s); }
+// Which kernel. Times in us, 128x128 tiles / 64x64 tiles / few rows:
+//   few rows (m up to 128, or 32 a group on average, by the buffer's rows):
+//     16 x 8192 x 5120        44 / 23 / 9.8      128 x 4096 x 4096   38 / 19 / 14.2
+//     64 groups, 1472 rows x 4096 x 2048  125 / 120 / 107
+//     against 256 x 4096 x 4096  39 / 20 / 28;   32 groups, 1504 rows x 2048 x 2048  35 / 37 / 46
+//   64x64 tiles up to 160 tiles of 128x128, where those leave CUs idle:
+//     777 x 1361 x 1999       24 / 17 / 24       512 x 4096 x 4096   40 / 29 / 52
+//     against 1024 x 4096 x 4096 (256 tiles)  46 / 56 / 103
+// 256x256 tiles (570 us at 8192 x 8192 x 5120, as 128x128 ones) lose by
+// groups (1168 against 1053 us at 64 groups, 73664 rows x 4096 x 2048).
+hipError_t launch_fp8_matmul(const Fp8Matmul &p, hipStream_t s) {
+  const bool few = p.mode == kDense ? p.m <= 128 : p.mode == kGroupedRows && p.m <= 32 * static_cast<uint64_t>(p.groups);
+  if (few) {
+    // a wave's share is best at least the four blocks that it asks for at once
+    if (p.kblocks >= 24) return launch_rows<8>(p, s);
+    if (p.kblocks >= 12) return launch_rows<4>(p, s);
+    if (p.kblocks >= 6) return launch_rows<2>(p, s);
+    return launch_rows<1>(p, s);
+  }
+  const uint64_t tiles = (static_cast<uint64_t>(p.m) + 127) / 128 * ((static_cast<uint64_t>(p.n) + 127) / 128) * (p.mode == kGroupedK ? p.groups : 1);
+  if (tiles <= 160) return launch_tile<64, 64, 2, 2, 4>(p, s);
+  return launch_tile<128, 128, 2, 2, 2>(p, s);
+}
 
 }  // namespace nvfp4
