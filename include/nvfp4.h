@@ -412,11 +412,13 @@ nvfp4_status_t nvfp4_expert_sort(const void *ids, uint32_t id_bytes, int64_t tok
 
 /*
  * Tokens to the sorted rows: y[r] = x[row_slots[r] / topk], zeros where
- * row_slots[r] is not a slot (0 .. tokens * topk - 1). x is [tokens][cols],
- * y [rows][cols], both of `dtype` and 16-byte aligned; any cols.
+ * row_slots[r] is not a slot (0 .. tokens * topk - 1). slot_rows and row_slots
+ * come from one sort (each other's inverse). x is [tokens][cols], y
+ * [rows][cols], both of `dtype` and 16-byte aligned; any cols.
  */
 nvfp4_status_t nvfp4_expert_gather(const void *x, nvfp4_dtype_t dtype, int64_t tokens, int64_t topk, int64_t cols,
-                                   const int32_t *row_slots, int64_t rows, void *y, void *stream);
+                                   const int32_t *slot_rows, const int32_t *row_slots, int64_t rows, void *y,
+                                   void *stream);
 
 /*
  * Sorted rows back to tokens: out[t] = sum over j of weights[t][j] *

@@ -152,7 +152,7 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
     lib.nvfp4_expert_sort.restype = I
     lib.nvfp4_expert_sort.argtypes = [P, U32, I64, I64, I64, I64, I64, P, P, P, P, P, P]
     lib.nvfp4_expert_gather.restype = I
-    lib.nvfp4_expert_gather.argtypes = [P, I, I64, I64, I64, P, I64, P, P]
+    lib.nvfp4_expert_gather.argtypes = [P, I, I64, I64, I64, P, P, I64, P, P]
     lib.nvfp4_expert_combine.restype = I
     lib.nvfp4_expert_combine.argtypes = [P, I, I64, I64, I64, P, I64, P, P, P]
     lib.nvfp4_expert_combine_grad.restype = I
@@ -587,8 +587,8 @@ def expert_gather(x: torch.Tensor, plan: ExpertPlan, *, stream=None) -> torch.Te
         with _under(stream, dev):
             return expert_gather(x, plan)
     y = torch.empty((plan.rows, x.shape[1]), dtype=x.dtype, device=dev)
-    _check(load().nvfp4_expert_gather(_ptr(x), code, plan.tokens, plan.topk, x.shape[1], _ptr(plan.row_slots), plan.rows,
-                                      _ptr(y), _current(dev)))
+    _check(load().nvfp4_expert_gather(_ptr(x), code, plan.tokens, plan.topk, x.shape[1], _ptr(plan.slot_rows),
+                                      _ptr(plan.row_slots), plan.rows, _ptr(y), _current(dev)))
     return y
 
 

@@ -700,16 +700,19 @@ extern "C" nvfp4_status_t nvfp4_expert_sort(const void *ids, uint32_t id_bytes, 
 }
 
 extern "C" nvfp4_status_t nvfp4_expert_gather(const void *x, nvfp4_dtype_t dtype, int64_t tokens, int64_t topk, int64_t cols,
-                                              const int32_t *row_slots, int64_t rows, void *y, void *stream) {
+                                              const int32_t *slot_rows, const int32_t *row_slots, int64_t rows, void *y,
+                                              void *stream) {
   nvfp4_status_t st = check_rows(dtype, tokens, topk, cols, rows);
   if (st != NVFP4_OK) return st;
   const bool empty = rows == 0 || cols == 0;
   if ((st = check_buffer(x, 16, empty || tokens == 0, "x")) != NVFP4_OK) return st;
+  if ((st = check_buffer(slot_rows, 4, empty || tokens == 0, "slot_rows")) != NVFP4_OK) return st;
   if ((st = check_buffer(row_slots, 4, empty, "row_slots")) != NVFP4_OK) return st;
   if ((st = check_buffer(y, 16, empty, "y")) != NVFP4_OK) return st;
   if (empty) return NVFP4_OK;
   nvfp4::ExpertRows p{};
   p.x = x;
+  p.slot_rows = slot_rows;
   p.row_slots = row_slots;
   p.tokens = static_cast<uint32_t>(tokens);
   p.topk = static_cast<uint32_t>(topk);

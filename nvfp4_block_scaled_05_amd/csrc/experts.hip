@@ -47,7 +47,7 @@ struct SortArgs {
   const void *ids;
   uint32_t wide;  // ids are 64-bit
   uint32_t slots, experts, align_log2;
-  uint32_t chunk, chunks;  // slots of a chunk (a multiple of the tile), chunks
+  uint32_t chunk, chunks;  // slots of a chunk, chunks
   uint32_t rounds;         // rounds of a wave in a tile
   uint32_t rows;
   int32_t *slot_rows, *row_slots, *offsets, *counts;
@@ -77,7 +77,7 @@ __global__ __launch_bounds__(kSortThreads) void k_expert_count(SortArgs a) {
 
 __global__ __launch_bounds__(kSortThreads) void k_expert_place(SortArgs a) {
   __shared__ uint32_t cnt[kSortWaves][kMaxKeys];  // a wave's slots of each key; then its first rank
-  __shared__ uint32_t total[kMaxKeys], next[kMaxKeys], start[kMaxKeys + 1];
+  __shared__ uint32_t total[kMaxKeys], next[kMaxKeys], start[kMaxKeys + 1], parts[kSortThreads / kMaxKeys][2][kMaxKeys];
   const uint32_t t = threadIdx.x, lane = t % kWave, wave = t / kWave;
   const uint64_t first = static_cast<uint64_t>(blockIdx.x) * a.chunk;
   const uint64_t last = min(first + a.chunk, static_cast<uint64_t>(a.slots));
@@ -116,21 +116,32 @@ __global__ __launch_bounds__(kSortThreads) void k_expert_place(SortArgs a) {
     __syncthreads();
     if (tile == first) {
       // totals, this chunk's first rank of each key, and the experts' first rows
-      if (t < kMaxKeys) {
+      if (a.hist == nullptr) {
+        if (t < kMaxKeys) {
+          uint32_t all = 0;
+#pragma unroll
+          for (uint32_t w = 0; w < kSortWaves; ++w) all += cnt[w][t];
+          total[t] = all;
+          next[t] = 0;
+        }
+      } else {  // four threads a key, each a quarter of the chunks
+        const uint32_t e = t % kMaxKeys, part = t / kMaxKeys;
         uint32_t mine = 0, all = 0;
-        if (t < a.experts) {
-          if (a.hist == nullptr) {
-            for (uint32_t w = 0; w < kSortWaves; ++w) all += cnt[w][t];
-          } else {
-            for (uint32_t c = 0; c < a.chunks; ++c) {
-              const uint32_t h = a.hist[c * a.experts + t];
-              all += h;
-              mine += c < blockIdx.x ? h : 0u;
-            }
+        if (e < a.experts) {
+#pragma unroll 8
+          for (uint32_t c = part; c < a.chunks; c += kSortThreads / kMaxKeys) {
+            const uint32_t h = a.hist[c * a.experts + e];
+            all += h;
+            mine += c < blockIdx.x ? h : 0u;
           }
         }
-        total[t] = all;
-        next[t] = mine;
+        parts[part][0][e] = all;
+        parts[part][1][e] = mine;
+        __syncthreads();
+        if (t < kMaxKeys) {
+          total[t] = parts[0][0][t] + parts[1][0][t] + parts[2][0][t] + parts[3][0][t];
+          next[t] = parts[0][1][t] + parts[1][1][t] + parts[2][1][t] + parts[3][1][t];
+        }
       }
       __syncthreads();
       if (wave == 0) {  // exclusive sum of the padded totals, four keys a lane
@@ -253,28 +264,59 @@ __device__ __forceinline__ void zero_row(typename Elem<DT>::type *dst, uint32_t 
   for (uint32_t c = cols / per * per + lane; c < cols; c += kWave) dst[c] = 0;
 }
 
-// One wave a row. Bound by bytes: each of the R rows is written once, each
-// token's row is read topk times, all but the first from a cache.
+// A row's pieces past the caches: rows that are written or read once.
+__device__ __forceinline__ void put(void *p, piece_t v) { __builtin_nontemporal_store(v, static_cast<piece_t *>(p)); }
+__device__ __forceinline__ piece_t take(const void *p) { return __builtin_nontemporal_load(static_cast<const piece_t *>(p)); }
+
+// Rows without a slot are cleared by waves of their own, kPadRows of them each.
+constexpr uint32_t kPadRows = 2;
+template <int DT>
+__device__ __forceinline__ void clear_padding(typename Elem<DT>::type *y, const int32_t *row_slots, uint64_t r0, uint32_t slots,
+                                              uint32_t cols, uint32_t rows, uint32_t lane) {
+  for (uint64_t r = r0; r < r0 + kPadRows && r < rows; ++r)
+    if (static_cast<uint32_t>(row_slots[r]) >= slots) zero_row<DT>(y + r * cols, cols, lane);
+}
+
+// One wave a token and 64 * kGatherPieces pieces of its columns, which it
+// writes to the rows of all its choices. Bound by bytes: each token's row is
+// read once, each sorted row written once.
+constexpr uint32_t kGatherPieces = 1;
 template <int DT>
 __global__ __launch_bounds__(kRowThreads) void k_expert_gather(const typename Elem<DT>::type *__restrict__ x,
-                                                               const int32_t *__restrict__ row_slots, uint32_t slots,
-                                                               uint32_t topk, uint32_t cols, uint32_t rows,
+                                                               const int32_t *__restrict__ slot_rows,
+                                                               const int32_t *__restrict__ row_slots, uint32_t tokens,
+                                                               uint32_t topk, uint32_t cols, uint32_t rows, uint32_t strips,
                                                                typename Elem<DT>::type *__restrict__ y) {
   constexpr uint32_t per = Elem<DT>::per;
   const uint32_t lane = threadIdx.x % kWave;
-  const uint32_t r = blockIdx.x * kRowWaves + wave_index();
-  if (r >= rows) return;
-  const uint32_t slot = static_cast<uint32_t>(row_slots[r]);
-  typename Elem<DT>::type *dst = y + static_cast<uint64_t>(r) * cols;
-  if (slot >= slots) {
-    zero_row<DT>(dst, cols, lane);
+  const uint64_t unit = static_cast<uint64_t>(blockIdx.x) * kRowWaves + wave_index(), units = static_cast<uint64_t>(tokens) * strips;
+  if (unit >= units) {
+    clear_padding<DT>(y, row_slots, (unit - units) * kPadRows, tokens * topk, cols, rows, lane);
     return;
   }
-  const typename Elem<DT>::type *src = x + static_cast<uint64_t>(slot / topk) * cols;
-#pragma unroll 4
-  for (uint32_t c = lane * per; c + per <= cols; c += kWave * per)
-    *reinterpret_cast<piece_t *>(dst + c) = *reinterpret_cast<const piece_t *>(src + c);
-  for (uint32_t c = cols / per * per + lane; c < cols; c += kWave) dst[c] = src[c];
+  const uint32_t token = static_cast<uint32_t>(unit / strips), strip = static_cast<uint32_t>(unit % strips);
+  const int32_t *at = slot_rows + static_cast<uint64_t>(token) * topk;
+  const typename Elem<DT>::type *src = x + static_cast<uint64_t>(token) * cols;
+  const uint32_t c0 = (strip * kGatherPieces * kWave + lane) * per;
+  piece_t v[kGatherPieces];
+  typename Elem<DT>::type rest[per];
+#pragma unroll
+  for (uint32_t i = 0; i < kGatherPieces; ++i) {
+    const uint32_t c = c0 + i * kWave * per;
+    if (c + per <= cols) v[i] = *reinterpret_cast<const piece_t *>(src + c);
+    else for (uint32_t q = 0; q < per; ++q) if (c + q < cols) rest[q] = src[c + q];  // one lane's, at most
+  }
+  for (uint32_t j = 0; j < topk; ++j) {
+    const uint32_t row = static_cast<uint32_t>(at[j]);
+    if (row >= rows) continue;
+    typename Elem<DT>::type *dst = y + static_cast<uint64_t>(row) * cols;
+#pragma unroll
+    for (uint32_t i = 0; i < kGatherPieces; ++i) {
+      const uint32_t c = c0 + i * kWave * per;
+      if (c + per <= cols) put(dst + c, v[i]);
+      else for (uint32_t q = 0; q < per; ++q) if (c + q < cols) dst[c + q] = rest[q];
+    }
+  }
 }
 
 // One wave a token and 64 pieces of its columns: the rows of its choices,
@@ -297,19 +339,19 @@ __global__ __launch_bounds__(kRowThreads) void k_expert_combine(const typename E
   typename Elem<DT>::type *dst = out + static_cast<uint64_t>(token) * cols + c;
   if (c + per <= cols) {
     float acc[per] = {};
-    for (uint32_t j0 = 0; j0 < topk; j0 += 4) {
-      piece_t v[4];
-      float f[4];
+    for (uint32_t j0 = 0; j0 < topk; j0 += 8) {
+      piece_t v[8];
+      float f[8];
 #pragma unroll
-      for (uint32_t i = 0; i < 4; ++i) {
+      for (uint32_t i = 0; i < 8; ++i) {
         const uint32_t row = j0 + i < topk ? static_cast<uint32_t>(at[j0 + i]) : rows;
         f[i] = row < rows ? (wt ? wt[j0 + i] : 1.0f) : 0.0f;
         v[i] = piece_t{0, 0, 0, 0};
-        if (row < rows) v[i] = *reinterpret_cast<const piece_t *>(y + static_cast<uint64_t>(row) * cols + c);
+        if (row < rows) v[i] = take(y + static_cast<uint64_t>(row) * cols + c);
         else f[i] = 0.0f;
       }
 #pragma unroll
-      for (uint32_t i = 0; i < 4; ++i) {
+      for (uint32_t i = 0; i < 8; ++i) {
         float e[per];
         Elem<DT>::unpack(v[i], e);
 #pragma unroll
@@ -332,8 +374,6 @@ __global__ __launch_bounds__(kRowThreads) void k_expert_combine(const typename E
 // Combine's gradients: one wave a slot reads dout's row and y's row, writes
 // dy's row and the slot's dot product (so dout's row is read topk times, by
 // neighbouring waves); the waves past the slots clear the padding rows of dy.
-constexpr uint32_t kPadRows = 8;  // rows that one wave looks through
-
 template <int DT>
 __global__ __launch_bounds__(kRowThreads) void k_expert_combine_grad(
     const typename Elem<DT>::type *__restrict__ dout, const typename Elem<DT>::type *__restrict__ y,
@@ -344,9 +384,7 @@ __global__ __launch_bounds__(kRowThreads) void k_expert_combine_grad(
   const uint32_t lane = threadIdx.x % kWave;
   const uint64_t unit = static_cast<uint64_t>(blockIdx.x) * kRowWaves + wave_index();
   if (unit >= slots) {
-    const uint64_t r0 = (unit - slots) * kPadRows;
-    for (uint64_t r = r0; r < r0 + kPadRows && r < rows; ++r)
-      if (static_cast<uint32_t>(row_slots[r]) >= slots) zero_row<DT>(dy + r * cols, cols, lane);
+    clear_padding<DT>(dy, row_slots, (unit - slots) * kPadRows, slots, cols, rows, lane);
     return;
   }
   const uint32_t slot = static_cast<uint32_t>(unit);
@@ -364,13 +402,13 @@ __global__ __launch_bounds__(kRowThreads) void k_expert_combine_grad(
   for (uint32_t c = lane * per; c + per <= cols; c += kWave * per) {
     float a[per], b[per];
     Elem<DT>::unpack(*reinterpret_cast<const piece_t *>(g + c), a);
-    Elem<DT>::unpack(*reinterpret_cast<const piece_t *>(v + c), b);
+    Elem<DT>::unpack(take(v + c), b);
 #pragma unroll
     for (uint32_t q = 0; q < per; ++q) {
       dot = __builtin_fmaf(a[q], b[q], dot);
       a[q] *= wt;
     }
-    *reinterpret_cast<piece_t *>(dst + c) = Elem<DT>::pack(a);
+    put(dst + c, Elem<DT>::pack(a));
   }
   for (uint32_t c = cols / per * per + lane; c < cols; c += kWave) {
     const float a = Elem<DT>::load(g + c);
@@ -382,9 +420,12 @@ __global__ __launch_bounds__(kRowThreads) void k_expert_combine_grad(
   if (lane == 0) dw[slot] = dot;
 }
 
+// Slots of a workgroup: one round of its waves, or more where that would
+// make over kSortChunks workgroups. (65536 slots, 64 experts: 17.4 us in 16
+// workgroups of four rounds, 9.6 us in 64.)
 uint64_t sort_chunk(uint64_t slots) {
   const uint64_t c = (slots + kSortChunks - 1) / kSortChunks;
-  return (c + kSortTile - 1) / kSortTile * kSortTile;
+  return (c + kSortThreads - 1) / kSortThreads * kSortThreads;
 }
 
 uint64_t blocks_of(uint64_t units, uint64_t per) { return (units + per - 1) / per; }
@@ -407,9 +448,9 @@ hipError_t launch_expert_sort(const ExpertSort &p, hipStream_t s) {
   a.row_slots = p.row_slots;
   a.offsets = p.offsets;
   a.counts = p.counts;
-  a.chunk = p.slots ? static_cast<uint32_t>(sort_chunk(p.slots)) : kSortTile;
-  a.chunks = p.slots ? static_cast<uint32_t>(blocks_of(p.slots, a.chunk)) : 1;
-  a.rounds = static_cast<uint32_t>(std::min<uint64_t>(kSortRounds, std::max<uint64_t>(1, blocks_of(p.slots, kSortThreads))));
+  a.chunk = p.slots > kSortTile ? static_cast<uint32_t>(sort_chunk(p.slots)) : kSortTile;
+  a.chunks = p.slots > kSortTile ? static_cast<uint32_t>(blocks_of(p.slots, a.chunk)) : 1;
+  a.rounds = static_cast<uint32_t>(std::min<uint64_t>(kSortRounds, std::max<uint64_t>(1, blocks_of(std::min(p.slots, a.chunk), kSortThreads))));
   a.hist = a.chunks > 1 ? p.workspace : nullptr;
   if (a.chunks > 1) {
     hipLaunchKernelGGL(k_expert_count, dim3(a.chunks), dim3(kSortThreads), 0, s, a);
@@ -423,8 +464,11 @@ hipError_t launch_expert_sort(const ExpertSort &p, hipStream_t s) {
 template <int DT>
 static hipError_t gather_t(const ExpertRows &p, hipStream_t s) {
   typedef typename Elem<DT>::type T;
-  hipLaunchKernelGGL((k_expert_gather<DT>), dim3(static_cast<uint32_t>(blocks_of(p.rows, kRowWaves))), dim3(kRowThreads), 0, s,
-                     static_cast<const T *>(p.x), p.row_slots, p.tokens * p.topk, p.topk, p.cols, p.rows, static_cast<T *>(p.out));
+  const uint32_t strips = static_cast<uint32_t>(blocks_of(p.cols, kGatherPieces * kWave * Elem<DT>::per));
+  const uint64_t units = static_cast<uint64_t>(p.tokens) * strips + blocks_of(p.rows, kPadRows);
+  hipLaunchKernelGGL((k_expert_gather<DT>), dim3(static_cast<uint32_t>(blocks_of(units, kRowWaves))), dim3(kRowThreads), 0, s,
+                     static_cast<const T *>(p.x), p.slot_rows, p.row_slots, p.tokens, p.topk, p.cols, p.rows, strips,
+                     static_cast<T *>(p.out));
   return hipGetLastError();
 }
 
