@@ -183,13 +183,25 @@ __device__ __forceinline__ Wide widen(u32x4 w) { return Wide{widen8(w.x, w.y), w
 // along k is one block of 128 bytes of every row; ST stages in LDS, filled by
 // loads straight to LDS while the matrix cores work on the oldest one.
 //
-// At 8192 x 8192 x 5120 this takes 570 us (1.2 PFLOP/s) in 128x128 tiles, two
-// workgroups a CU. The widening and the scaling are 3 vector instructions
-// for each v_mfma; measured alone, a v_mfma takes 17 cycles with up to two
-// of them beside it and 22 with three, and the mix of this kernel from
+// At 8192 x 8192 x 5120 this takes 570 to 600 us (1.2 PFLOP/s, by the box) in
+// 128x128 tiles, two workgroups a CU. The widening and the scaling are 3 vector
+// instructions for each v_mfma; measured alone, a v_mfma takes 17 cycles with up
+// to two of them beside it and 22 with three, and the mix of this kernel from
 // registers only 25, against 29 here. The rest is power: the clock drops to
 // 2.1 GHz. 32x32x16 v_mfma, which leave more room beside them, need 5% fewer
 // cycles and take 590 us, at 1.9 GHz.
+//
+// PHASED: 256x256 tiles, waves of 128x64, which widen and read LDS less (2.5
+// vector instructions a v_mfma), but one workgroup a CU, whose waves would all
+// wait, then read and widen b, and leave the matrix cores idle together: 570
+// us. So the two waves of each SIMD run half a step apart. Waves 0 .. 3 (upper
+// half of the rows) begin a step at one barrier and pass the next one in the
+// middle of it, where waves 4 .. 7 begin theirs: 535 to 545 us (1.27 PFLOP/s).
+// What that needs of the two stages: each half of the waves loads its own rows
+// of a, at its own steps' beginnings; b is read at a step's beginning only, so
+// the stage that the lower half has read by the middle of its step k, which is
+// where the upper half begins step k + 1, takes b of step k + 2 then, loaded by
+// the upper half. Each load has a whole step's time.
 //
 // LDS layout: rows of 128 bytes, eight 16-byte chunks, chunk g of row r at
 // place g ^ f(r), so that lanes that read one chunk of neighbouring rows meet
@@ -205,7 +217,7 @@ __device__ __forceinline__ Wide widen(u32x4 w) { return Wide{widen8(w.x, w.y), w
 template <uint32_t G>
 __device__ __forceinline__ uint32_t swizzle_b(uint32_t r) { return (r & 3) | (r / (4 * G) & 1) << 2; }
 
-template <uint32_t BM, uint32_t BN, uint32_t WM, uint32_t WN, uint32_t ST, bool SBV, bool OUT32>
+template <uint32_t BM, uint32_t BN, uint32_t WM, uint32_t WN, uint32_t ST, bool PHASED, bool SBV, bool OUT32>
 __global__ __launch_bounds__(WM *WN *kWave) void k_fp8_tile(Args p) {
   constexpr uint32_t kWaves = WM * WN;
   constexpr uint32_t TM = BM / WM, TN = BN / WN, MI = TM / 16, NI = TN / 16;
@@ -214,6 +226,8 @@ __global__ __launch_bounds__(WM *WN *kWave) void k_fp8_tile(Args p) {
   constexpr uint32_t kGroups = (BM + BN) / 64, kLoadS = (kGroups + kWaves - 1) / kWaves, kLoads = kLoadA + kLoadB + kLoadS;
   static_assert((NI == 2 || NI % 4 == 0) && BM % (8 * kWaves) == 0 && BN % (8 * kWaves) == 0, "tile shape");
   static_assert((ST - 2) * kLoads < 64, "loads in flight");
+  constexpr uint32_t kTurn = 3;  // of a phased wave's 8 row tiles, those before the barrier; 4: 2% slower, 2: 4%
+  static_assert(!PHASED || (BM == 256 && BN == 256 && WM == 2 && WN == 4 && ST == 2), "phased shape");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[ST][(BM + BN) * kBlock];
   __shared__ __attribute__((aligned(16))) float scales[ST][BM + BN];
 
@@ -244,24 +258,26 @@ __global__ __launch_bounds__(WM *WN *kWave) void k_fp8_tile(Args p) {
 
   // where this lane's share of each load comes from: rows past the end repeat the last one
   const uint32_t chunk = lane % 8;
-  uint32_t from_a[kLoadA], from_b[kLoadB];
+  const uint32_t phase = PHASED ? wave / (kWaves / 2) : 0, quarter = wave % (kWaves / 2);
+  uint32_t from_a[kLoadA], from_b[PHASED ? 2 : kLoadB];
 #pragma unroll
   for (uint32_t i = 0; i < kLoadA; ++i) {
     const uint32_t r = (wave * kLoadA + i) * 8 + lane / 8;
     from_a[i] = min(r, part.m_end - 1 - m0) * static_cast<uint32_t>(pitch) + ((chunk ^ (r & 7)) << 4);
   }
 #pragma unroll
-  for (uint32_t i = 0; i < kLoadB; ++i) {
-    const uint32_t r = (wave * kLoadB + i) * 8 + lane / 8;
+  for (uint32_t i = 0; i < (PHASED ? 2 : kLoadB); ++i) {
+    // (phased: n is a multiple of BN, and rows 16 i .. 16 i + 15 follow each other by whole pitches but for the swizzle)
+    const uint32_t r = PHASED ? quarter * kLoadB * 16 + i * 16 + lane / 8 : (wave * kLoadB + i) * 8 + lane / 8;
     from_b[i] = min(r, p.n - 1 - n0) * static_cast<uint32_t>(pitch) + ((chunk ^ swizzle_b<G>(r)) << 4);
   }
   if (SBV) sb += n0;
   // scales: 64 at a time, of 64 rows of a or of b; of b in 128x128 blocks, 64 times its block's.
   // Every wave makes as many loads, some of them twice, so that each can count its own.
-  uint32_t from_s[kLoadS];
+  uint32_t from_s[PHASED ? 2 : kLoadS];
 #pragma unroll
-  for (uint32_t i = 0; i < kLoadS; ++i) {
-    const uint32_t w = (wave * kLoadS + i) % kGroups, r = (w < BM / 64 ? w : w - BM / 64) * 64 + lane;
+  for (uint32_t i = 0; i < (PHASED ? 2 : kLoadS); ++i) {
+    const uint32_t w = PHASED ? (i == 0 ? phase * (BM / 128) + quarter % (BM / 128) : BM / 64 + quarter) : (wave * kLoadS + i) % kGroups, r = (w < BM / 64 ? w : w - BM / 64) * 64 + lane;
     from_s[i] = 4 * (w < BM / 64 ? min(r, part.m_end - 1 - m0) : SBV ? min(r, p.n - 1 - n0) : min((n0 + r) / kBlock, p.sb_stride - 1));
   }
 
@@ -272,16 +288,22 @@ __global__ __launch_bounds__(WM *WN *kWave) void k_fp8_tile(Args p) {
 #pragma unroll
     for (uint32_t i = 0; i < kLoadA; ++i) load16_to_lds(to + (wave * kLoadA + i) * 1024, ka, from_a[i]);
 #pragma unroll
-    for (uint32_t i = 0; i < kLoadB; ++i) load16_to_lds(to + BM * kBlock + (wave * kLoadB + i) * 1024, kbp, from_b[i]);
+    for (uint32_t i = 0; i < (PHASED ? 0 : kLoadB); ++i) load16_to_lds(to + BM * kBlock + (wave * kLoadB + i) * 1024, kbp, from_b[i]);
+    if (PHASED && phase == 0) {
 #pragma unroll
-    for (uint32_t i = 0; i < kLoadS; ++i) {
-      const uint32_t w = (wave * kLoadS + i) % kGroups;
+      for (uint32_t i = 0; i < 2 * kLoadB; ++i)
+        load16_to_lds(to + BM * kBlock + (quarter * 2 * kLoadB + i) * 1024, kbp + (i / 4 * 32 + i % 2 * 8) * pitch, from_b[i / 2 % 2]);
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < (PHASED ? 2 : kLoadS); ++i) {
+      const uint32_t w = PHASED ? (i == 0 ? phase * (BM / 128) + quarter % (BM / 128) : BM / 64 + quarter) : (wave * kLoadS + i) % kGroups;
+      if (PHASED && (i == 0 ? quarter >= BM / 128 : phase == 1)) continue;
       load4_to_lds(lds_scales + stage * static_cast<uint32_t>(sizeof scales[0]) + w * 256,
                    w < BM / 64 ? sa + static_cast<uint64_t>(kb) * p.sa_stride : sb + static_cast<uint64_t>(kb) * p.sb_stride, from_s[i]);
     }
   };
 
-  const uint32_t wm = wave % WM, wn = wave / WM;
+  const uint32_t wm = PHASED ? phase : wave % WM, wn = PHASED ? quarter : wave / WM;
   const uint32_t i16 = lane % 16, q = lane / 16;
   f32x4 acc[MI][NI];
 #pragma unroll
@@ -315,6 +337,7 @@ __global__ __launch_bounds__(WM *WN *kWave) void k_fp8_tile(Args p) {
     }
 #pragma unroll
     for (uint32_t i = 0; i < MI; ++i) {
+      if (PHASED && i == kTurn) lds_barrier();
       const Wide a0 = widen(chunk_at(la, i * 16 + i16, q, i16 & 7)), a1 = widen(chunk_at(la, i * 16 + i16, q + 4, i16 & 7));
       const float s = ls[i * 16 + i16];
 #pragma unroll
@@ -332,6 +355,7 @@ __global__ __launch_bounds__(WM *WN *kWave) void k_fp8_tile(Args p) {
   if (!part.zero && part.kb0 < part.kb_end) {
 #pragma unroll
     for (uint32_t i = 0; i + 1 < ST; ++i) load(min(part.kb0 + i, part.kb_end - 1), i);
+    if (PHASED && phase == 1) lds_barrier();
     uint32_t stage = 0;
     for (uint32_t kb = part.kb0; kb < part.kb_end; ++kb) {
       wait_loads<(ST - 2) * kLoads>();  // this step's loads are in,
@@ -341,6 +365,7 @@ __global__ __launch_bounds__(WM *WN *kWave) void k_fp8_tile(Args p) {
       step(stage);
       stage = stage + 1 == ST ? 0 : stage + 1;
     }
+    if (PHASED && phase == 0) lds_barrier();
     if (ST > 2) wait_loads<0>();  // nothing writes to LDS after the end
   }
 
@@ -518,7 +543,7 @@ hipError_t launch_rows(const Fp8Matmul &p, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <uint32_t BM, uint32_t BN, uint32_t WM, uint32_t WN, uint32_t ST>
+template <uint32_t BM, uint32_t BN, uint32_t WM, uint32_t WN, uint32_t ST, bool PHASED = false>
 hipError_t launch_tile(const Fp8Matmul &p, hipStream_t s) {
   Args a{p.a, p.b, p.sa, p.sb, p.d, p.m, p.n, p.kblocks, p.sa_stride, p.sb_stride, p.mode, p.offsets, p.groups, 0, 0};
   a.tiles_n = (p.n + BN - 1) / BN;
@@ -531,11 +556,11 @@ hipError_t launch_tile(const Fp8Matmul &p, hipStream_t s) {
   if (blocks >= (uint64_t{1} << 31)) return hipErrorInvalidConfiguration;
   const dim3 grid(static_cast<uint32_t>(blocks)), threads(WM * WN * kWave);
   if (p.b_block_2d) {
-    if (p.out_fp32) hipLaunchKernelGGL((k_fp8_tile<BM, BN, WM, WN, ST, false, true>), grid, threads, 0, s, a);
-    else hipLaunchKernelGGL((k_fp8_tile<BM, BN, WM, WN, ST, false, false>), grid, threads, 0, s, a);
+    if (p.out_fp32) hipLaunchKernelGGL((k_fp8_tile<BM, BN, WM, WN, ST, PHASED, false, true>), grid, threads, 0, s, a);
+    else hipLaunchKernelGGL((k_fp8_tile<BM, BN, WM, WN, ST, PHASED, false, false>), grid, threads, 0, s, a);
   } else {
-    if (p.out_fp32) hipLaunchKernelGGL((k_fp8_tile<BM, BN, WM, WN, ST, true, true>), grid, threads, 0, s, a);
-    else hipLaunchKernelGGL((k_fp8_tile<BM, BN, WM, WN, ST, true, false>), grid, threads, 0, s, a);
+    if (p.out_fp32) hipLaunchKernelGGL((k_fp8_tile<BM, BN, WM, WN, ST, PHASED, true, true>), grid, threads, 0, s, a);
+    else hipLaunchKernelGGL((k_fp8_tile<BM, BN, WM, WN, ST, PHASED, true, false>), grid, threads, 0, s, a);
   }
   return hipGetLastError();
 }
@@ -550,8 +575,13 @@ hipError_t launch_tile(const Fp8Matmul &p, hipStream_t s) {
 //   64x64 tiles up to 160 tiles of 128x128, where those leave CUs idle:
 //     777 x 1361 x 1999       24 / 17 / 24       512 x 4096 x 4096   40 / 29 / 52
 //     against 1024 x 4096 x 4096 (256 tiles)  46 / 56 / 103
-// 256x256 tiles (570 us at 8192 x 8192 x 5120, as 128x128 ones) lose by
-// groups (1168 against 1053 us at 64 groups, 73664 rows x 4096 x 2048).
+//   256x256 tiles where their rounds over 256 CUs, 3.2 us a step along k, take
+//   less than those of 128x128 tiles over 512 places, 1.8 us a step (times 128x128 / 256x256):
+//     8192 x 8192 x 5120      600 / 543          4096 x 4096 x 4096  132 / 117
+//     8 groups, 66552 rows x 4096 x 2048  1007 / 939
+//     against 3000 x 8192 x 5120  229 / 253;     16 groups, 34800 rows x 2048 x 4096  519 / 528
+//   By groups along k those are short, and 256x256 tiles lose (762 / 843 for
+//   32 groups, 4096 x 2048 x about 1100).
 hipError_t launch_fp8_matmul(const Fp8Matmul &p, hipStream_t s) {
   const bool few = p.mode == kDense ? p.m <= 128 : p.mode == kGroupedRows && p.m <= 32 * static_cast<uint64_t>(p.groups);
   if (few) {
@@ -561,8 +591,15 @@ hipError_t launch_fp8_matmul(const Fp8Matmul &p, hipStream_t s) {
     if (p.kblocks >= 6) return launch_rows<2>(p, s);
     return launch_rows<1>(p, s);
   }
-  const uint64_t tiles = (static_cast<uint64_t>(p.m) + 127) / 128 * ((static_cast<uint64_t>(p.n) + 127) / 128) * (p.mode == kGroupedK ? p.groups : 1);
+  // by groups of rows, every second group's last tile is taken to be a partial one
+  auto count = [&](uint64_t edge) {
+    const uint64_t rows = (p.m + edge - 1) / edge + (p.mode == kGroupedRows ? p.groups / 2 : 0);
+    return rows * ((p.n + edge - 1) / edge) * (p.mode == kGroupedK ? p.groups : 1);
+  };
+  const uint64_t tiles = count(128);
   if (tiles <= 160) return launch_tile<64, 64, 2, 2, 4>(p, s);
+  if (p.mode != kGroupedK && p.n % 256 == 0 && 64 * ((count(256) + 255) / 256) <= 35 * ((tiles + 511) / 512))
+    return launch_tile<256, 256, 2, 4, 2, true>(p, s);
   return launch_tile<128, 128, 2, 2, 2>(p, s);
 }
 

@@ -140,6 +140,44 @@ def test_matmul(m, n, k, b_2d, out):
     H.close(d, want, bound)
 
 
+def on_device(q, b=None):
+    """vals() on the device."""
+    data, scales = (q.data, q.scales) if b is None else (q.data[b], q.scales[b])
+    s = scales.double().t().repeat_interleave(128, 1)
+    if q.block_2d:
+        s = s.repeat_interleave(128, 0)[:data.shape[0]]
+    return data.float().double() * s
+
+
+def check_on_device(d, a, b):
+    """d against H.product of a and b (binary64 on the device): for sizes that would take long on the host."""
+    bound = (a.abs() @ b.abs().t()) * (128 * 2.0 ** -23 + (max(1, a.shape[1] // 128) + 2) * 2.0 ** -24)
+    H.close(d, H.f64(a @ b.t()), H.f64(bound))
+
+
+# sizes whose outputs take 256x256 tiles, whole and partial, few and many steps along k; then 128x128 ones
+@pytest.mark.parametrize("m,n,k", [(4096, 4096, 128), (4033, 4096, 256), (2050, 8192, 384), (6000, 2560, 1000), (4096, 4096, 2176),
+                                   (4096, 4095, 700), (2100, 4100, 130)])
+@pytest.mark.parametrize("b_2d,out", [(True, torch.bfloat16), (False, torch.float32)])
+def test_matmul_large(m, n, k, b_2d, out):
+    a, b = operand(m, k, False, m + k), operand(n, k, b_2d, n + 2 * k)
+    check_on_device(nv.fp8_matmul(a, b, out_dtype=out), on_device(a), on_device(b))
+
+
+@pytest.mark.parametrize("counts,align", [([3000, 0, 1300, 2049, 5], 128), ([2500, 1700, 3000], 1), ([1000] * 9, 16)])
+def test_matmul_grouped_large(counts, align):
+    n, k = 4096, 300
+    plan = plan_of(counts, align, drop=70)
+    a, _ = nv.fp8_quantize(rand((plan.tokens, k), torch.float32, 1, spread=1.0), plan=plan)
+    b = operand(n, k, True, 2, lead=(len(counts),))
+    d = nv.fp8_matmul_grouped(a, b, plan)
+    va, off = on_device(a), H.i64(plan.offsets)
+    for e in range(len(counts)):
+        r = slice(off[e], off[e + 1])
+        check_on_device(d[r], va[r], on_device(b, e))
+    assert not bool(d[off[-1]:].any())
+
+
 @pytest.mark.parametrize("m", [1, 40, 600])
 def test_matmul_keeps_exact_sums_exact(m):
     # whole numbers below 2^24 in every partial sum, and scales that are powers of two
