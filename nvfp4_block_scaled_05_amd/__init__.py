@@ -565,14 +565,13 @@ def expert_sort(ids: torch.Tensor, experts: int, *, align: int = FP8_BLOCK, rows
     if stream is not None:
         with _under(stream, dev):
             return expert_sort(ids, experts, align=align, rows=rows)
-    n = lib.nvfp4_expert_sort_workspace_bytes(tokens, topk, experts)
-    slot_rows = torch.empty((tokens, topk), dtype=torch.int32, device=dev)
-    row_slots = torch.empty((max(rows, 0),), dtype=torch.int32, device=dev)
-    offsets = torch.empty((max(experts, 0) + 1,), dtype=torch.int32, device=dev)
-    counts = torch.empty((max(experts, 0),), dtype=torch.int32, device=dev)
-    ws = torch.empty((n,), dtype=torch.uint8, device=dev) if n else None
+    # one allocation for all five arrays (each costs more than cutting them apart)
+    sizes = (tokens * topk, max(rows, 0), max(experts, 0) + 1, max(experts, 0),
+             lib.nvfp4_expert_sort_workspace_bytes(tokens, topk, experts) // 4)
+    slot_rows, row_slots, offsets, counts, ws = torch.split_with_sizes(ids.new_empty((sum(sizes),), dtype=torch.int32), sizes)
+    slot_rows = slot_rows.view(tokens, topk)
     _check(lib.nvfp4_expert_sort(_ptr(ids), ids.element_size(), tokens, topk, experts, align, rows, _ptr(slot_rows),
-                                 _ptr(row_slots), _ptr(offsets), _ptr(counts), _ptr(ws), _current(dev)))
+                                 _ptr(row_slots), _ptr(offsets), _ptr(counts), _ptr(ws) if sizes[4] else None, _current(dev)))
     return ExpertPlan(slot_rows, row_slots, offsets, counts, align)
 
 

@@ -211,7 +211,9 @@ __device__ __forceinline__ Wide widen(u32x4 w) { return Wide{widen8(w.x, w.y), w
 // row l % 16 of a, four consecutive rows 4 (l / 16) .. of the 16x16 tile's
 // b. Which rows of b a tile takes is free: tile j of G takes rows 4 G q + 4 j
 // + r of a group of 16 G as its rows 4 q + r, so that a lane ends with 4 G
-// consecutive columns of d and stores 16 bytes at a time.
+// consecutive columns of d: 16 bytes, which four lanes continue to 64. (With
+// G 4 a store is 16 bytes of every 64; the FP32 weight gradients of 32 groups,
+// 4096 x 2048 each, took 780 us so, and take 711.)
 // ---------------------------------------------------------------------------
 // f(r) of b: with that order of its rows, eight lanes that follow each other get eight values
 template <uint32_t G>
@@ -221,7 +223,8 @@ template <uint32_t BM, uint32_t BN, uint32_t WM, uint32_t WN, uint32_t ST, bool 
 __global__ __launch_bounds__(WM *WN *kWave) void k_fp8_tile(Args p) {
   constexpr uint32_t kWaves = WM * WN;
   constexpr uint32_t TM = BM / WM, TN = BN / WN, MI = TM / 16, NI = TN / 16;
-  constexpr uint32_t G = NI < 4 ? NI : 4, NG = NI / G;  // 16-row tiles of b that share 16 G rows
+  constexpr uint32_t G = OUT32 ? 1 : 2, NG = NI / G;  // 16-row tiles of b that share 16 G rows
+  constexpr uint32_t NS = NI < 4 ? 1 : NI / 4;        // scales of b in 128x128 blocks, for 64 columns each
   constexpr uint32_t kLoadA = BM / 8 / kWaves, kLoadB = BN / 8 / kWaves;  // loads of 8 rows that a wave makes
   constexpr uint32_t kGroups = (BM + BN) / 64, kLoadS = (kGroups + kWaves - 1) / kWaves, kLoads = kLoadA + kLoadB + kLoadS;
   static_assert((NI == 2 || NI % 4 == 0) && BM % (8 * kWaves) == 0 && BN % (8 * kWaves) == 0, "tile shape");
@@ -267,8 +270,8 @@ __global__ __launch_bounds__(WM *WN *kWave) void k_fp8_tile(Args p) {
   }
 #pragma unroll
   for (uint32_t i = 0; i < (PHASED ? 2 : kLoadB); ++i) {
-    // (phased: n is a multiple of BN, and rows 16 i .. 16 i + 15 follow each other by whole pitches but for the swizzle)
-    const uint32_t r = PHASED ? quarter * kLoadB * 16 + i * 16 + lane / 8 : (wave * kLoadB + i) * 8 + lane / 8;
+    // (phased: n is a multiple of BN, and rows go up by whole pitches; by G the swizzle may take turns every eight rows)
+    const uint32_t r = PHASED ? (quarter * 2 * kLoadB + i) * 8 + lane / 8 : (wave * kLoadB + i) * 8 + lane / 8;
     from_b[i] = min(r, p.n - 1 - n0) * static_cast<uint32_t>(pitch) + ((chunk ^ swizzle_b<G>(r)) << 4);
   }
   if (SBV) sb += n0;
@@ -292,7 +295,7 @@ __global__ __launch_bounds__(WM *WN *kWave) void k_fp8_tile(Args p) {
     if (PHASED && phase == 0) {
 #pragma unroll
       for (uint32_t i = 0; i < 2 * kLoadB; ++i)
-        load16_to_lds(to + BM * kBlock + (quarter * 2 * kLoadB + i) * 1024, kbp + (i / 4 * 32 + i % 2 * 8) * pitch, from_b[i / 2 % 2]);
+        load16_to_lds(to + BM * kBlock + (quarter * 2 * kLoadB + i) * 1024, kbp + (G == 1 ? i : i / 2 * 2) * 8 * pitch, from_b[G == 1 ? 0 : i % 2]);
     }
 #pragma unroll
     for (uint32_t i = 0; i < (PHASED ? 2 : kLoadS); ++i) {
@@ -320,10 +323,10 @@ __global__ __launch_bounds__(WM *WN *kWave) void k_fp8_tile(Args p) {
   auto step = [&](uint32_t stage) {
     const uint8_t *la = &lds[stage][wm * TM * kBlock], *lb = &lds[stage][(BM + wn * TN) * kBlock];
     const float *ls = &scales[stage][wm * TM], *lsb = &scales[stage][BM + wn * TN];
-    float sbu[NG];
+    float sbu[NS];
     if (!SBV) {
 #pragma unroll
-      for (uint32_t g = 0; g < NG; ++g) sbu[g] = lsb[16 * G * g];
+      for (uint32_t g = 0; g < NS; ++g) sbu[g] = lsb[64 * g];
     }
     Wide b0[NI], b1[NI];
     f32x4 sbv[NI];
@@ -347,7 +350,7 @@ __global__ __launch_bounds__(WM *WN *kWave) void k_fp8_tile(Args p) {
         c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b1[j].lo, a1.lo, c, 0, 0, 0);
         c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b1[j].hi, a1.hi, c, 0, 0, 0);
 #pragma unroll
-        for (uint32_t e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(c[e], SBV ? s * sbv[j][e] : s * sbu[j / G], acc[i][j][e]);
+        for (uint32_t e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(c[e], SBV ? s * sbv[j][e] : s * sbu[j / 4], acc[i][j][e]);
       }
     }
   };
