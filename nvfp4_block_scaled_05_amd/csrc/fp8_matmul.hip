@@ -146,7 +146,7 @@ __device__ __forceinline__ void store(void *d, uint64_t row, uint32_t j, uint32_
 // Loads straight to LDS, 16 bytes or 4 a lane: lane l's go to `to` + 16 l (4 l),
 // from `from` + `offset`. Written out, since the compiler waits for every
 // such load before the next LDS read, whichever stage it reads. They have no
-// destination register; wait_loads() waits until at most LEFT are on their way.
+// destination register; wait_loads() waits for all of them.
 __device__ __forceinline__ uint32_t lds_address(const void *p) {
   return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const void *)p));
 }
@@ -161,10 +161,7 @@ __device__ __forceinline__ void load4_to_lds(uint32_t to, const void *from, uint
   asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %2, %3\n\ts_mov_b32 m0, %0"
                : "=&s"(keep) : "s"(to), "v"(offset), "s"(from) : "memory");
 }
-template <uint32_t LEFT>
-__device__ __forceinline__ void wait_loads() {
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LEFT) : "memory");
-}
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // 16 codes to BF16: the eight of the first two words and of the last two.
 struct Wide {
@@ -180,8 +177,10 @@ __device__ __forceinline__ Wide widen(u32x4 w) { return Wide{widen8(w.x, w.y), w
 
 // ---------------------------------------------------------------------------
 // Tiles of BM x BN, WM x WN waves, each wave (BM / WM) x (BN / WN). A step
-// along k is one block of 128 bytes of every row; ST stages in LDS, filled by
-// loads straight to LDS while the matrix cores work on the oldest one.
+// along k is one block of 128 bytes of every row; two stages in LDS, the next
+// one filled by loads straight to LDS while the matrix cores work on this one.
+// KS times as many waves may share a tile, each share with every KS-th block,
+// stages and accumulators of its own, which are added up at the end.
 //
 // At 8192 x 8192 x 5120 this takes 570 to 600 us (1.2 PFLOP/s, by the box) in
 // 128x128 tiles, two workgroups a CU. The widening and the scaling are 3 vector
@@ -219,22 +218,22 @@ __device__ __forceinline__ Wide widen(u32x4 w) { return Wide{widen8(w.x, w.y), w
 template <uint32_t G>
 __device__ __forceinline__ uint32_t swizzle_b(uint32_t r) { return (r & 3) | (r / (4 * G) & 1) << 2; }
 
-template <uint32_t BM, uint32_t BN, uint32_t WM, uint32_t WN, uint32_t ST, bool PHASED, bool SBV, bool OUT32>
-__global__ __launch_bounds__(WM *WN *kWave) void k_fp8_tile(Args p) {
+template <uint32_t BM, uint32_t BN, uint32_t WM, uint32_t WN, uint32_t KS, bool PHASED, bool SBV, bool OUT32>
+__global__ __launch_bounds__(WM *WN *KS *kWave) void k_fp8_tile(Args p) {
   constexpr uint32_t kWaves = WM * WN;
   constexpr uint32_t TM = BM / WM, TN = BN / WN, MI = TM / 16, NI = TN / 16;
   constexpr uint32_t G = OUT32 ? 1 : 2, NG = NI / G;  // 16-row tiles of b that share 16 G rows
   constexpr uint32_t NS = NI < 4 ? 1 : NI / 4;        // scales of b in 128x128 blocks, for 64 columns each
   constexpr uint32_t kLoadA = BM / 8 / kWaves, kLoadB = BN / 8 / kWaves;  // loads of 8 rows that a wave makes
-  constexpr uint32_t kGroups = (BM + BN) / 64, kLoadS = (kGroups + kWaves - 1) / kWaves, kLoads = kLoadA + kLoadB + kLoadS;
+  constexpr uint32_t kGroups = (BM + BN) / 64, kLoadS = (kGroups + kWaves - 1) / kWaves;
   static_assert((NI == 2 || NI % 4 == 0) && BM % (8 * kWaves) == 0 && BN % (8 * kWaves) == 0, "tile shape");
-  static_assert((ST - 2) * kLoads < 64, "loads in flight");
   constexpr uint32_t kTurn = 3;  // of a phased wave's 8 row tiles, those before the barrier; 4: 2% slower, 2: 4%
-  static_assert(!PHASED || (BM == 256 && BN == 256 && WM == 2 && WN == 4 && ST == 2), "phased shape");
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[ST][(BM + BN) * kBlock];
-  __shared__ __attribute__((aligned(16))) float scales[ST][BM + BN];
+  static_assert(!PHASED || (BM == 256 && BN == 256 && WM == 2 && WN == 4 && KS == 1), "phased shape");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[KS][2][(BM + BN) * kBlock];
+  __shared__ __attribute__((aligned(16))) float scales[KS][2][BM + BN];
 
-  const uint32_t lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const uint32_t lane = threadIdx.x % kWave, any_wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const uint32_t wave = any_wave % kWaves, share = any_wave / kWaves;  // of the waves that share a tile's blocks along k
   uint32_t tm, tn;
   tile_of(blockIdx.x, p, tm, tn);
   Part part{tm * BM, p.m, 0, p.kblocks, 0, false};
@@ -276,7 +275,7 @@ __global__ __launch_bounds__(WM *WN *kWave) void k_fp8_tile(Args p) {
   }
   if (SBV) sb += n0;
   // scales: 64 at a time, of 64 rows of a or of b; of b in 128x128 blocks, 64 times its block's.
-  // Every wave makes as many loads, some of them twice, so that each can count its own.
+  // (Where there are more waves than that, some load the same again.)
   uint32_t from_s[PHASED ? 2 : kLoadS];
 #pragma unroll
   for (uint32_t i = 0; i < (PHASED ? 2 : kLoadS); ++i) {
@@ -284,10 +283,10 @@ __global__ __launch_bounds__(WM *WN *kWave) void k_fp8_tile(Args p) {
     from_s[i] = 4 * (w < BM / 64 ? min(r, part.m_end - 1 - m0) : SBV ? min(r, p.n - 1 - n0) : min((n0 + r) / kBlock, p.sb_stride - 1));
   }
 
-  const uint32_t lds_data = lds_address(&lds[0][0]), lds_scales = lds_address(&scales[0][0]);
+  const uint32_t lds_data = lds_address(&lds[share][0][0]), lds_scales = lds_address(&scales[share][0][0]);
   auto load = [&](uint32_t kb, uint32_t stage) {
     const uint8_t *ka = a + static_cast<uint64_t>(kb) * kBlock, *kbp = b + static_cast<uint64_t>(kb) * kBlock;
-    const uint32_t to = lds_data + stage * static_cast<uint32_t>(sizeof lds[0]);
+    const uint32_t to = lds_data + stage * static_cast<uint32_t>(sizeof lds[0][0]);
 #pragma unroll
     for (uint32_t i = 0; i < kLoadA; ++i) load16_to_lds(to + (wave * kLoadA + i) * 1024, ka, from_a[i]);
 #pragma unroll
@@ -301,7 +300,7 @@ __global__ __launch_bounds__(WM *WN *kWave) void k_fp8_tile(Args p) {
     for (uint32_t i = 0; i < (PHASED ? 2 : kLoadS); ++i) {
       const uint32_t w = PHASED ? (i == 0 ? phase * (BM / 128) + quarter % (BM / 128) : BM / 64 + quarter) : (wave * kLoadS + i) % kGroups;
       if (PHASED && (i == 0 ? quarter >= BM / 128 : phase == 1)) continue;
-      load4_to_lds(lds_scales + stage * static_cast<uint32_t>(sizeof scales[0]) + w * 256,
+      load4_to_lds(lds_scales + stage * static_cast<uint32_t>(sizeof scales[0][0]) + w * 256,
                    w < BM / 64 ? sa + static_cast<uint64_t>(kb) * p.sa_stride : sb + static_cast<uint64_t>(kb) * p.sb_stride, from_s[i]);
     }
   };
@@ -321,8 +320,8 @@ __global__ __launch_bounds__(WM *WN *kWave) void k_fp8_tile(Args p) {
   };
 
   auto step = [&](uint32_t stage) {
-    const uint8_t *la = &lds[stage][wm * TM * kBlock], *lb = &lds[stage][(BM + wn * TN) * kBlock];
-    const float *ls = &scales[stage][wm * TM], *lsb = &scales[stage][BM + wn * TN];
+    const uint8_t *la = &lds[share][stage][wm * TM * kBlock], *lb = &lds[share][stage][(BM + wn * TN) * kBlock];
+    const float *ls = &scales[share][stage][wm * TM], *lsb = &scales[share][stage][BM + wn * TN];
     float sbu[NS];
     if (!SBV) {
 #pragma unroll
@@ -356,20 +355,39 @@ __global__ __launch_bounds__(WM *WN *kWave) void k_fp8_tile(Args p) {
   };
 
   if (!part.zero && part.kb0 < part.kb_end) {
-#pragma unroll
-    for (uint32_t i = 0; i + 1 < ST; ++i) load(min(part.kb0 + i, part.kb_end - 1), i);
+    // (a share without a block in the last round loads the last one and leaves it)
+    const uint32_t last = part.kb_end - 1;
+    load(min(part.kb0 + share, last), 0);
     if (PHASED && phase == 1) lds_barrier();
     uint32_t stage = 0;
-    for (uint32_t kb = part.kb0; kb < part.kb_end; ++kb) {
-      wait_loads<(ST - 2) * kLoads>();  // this step's loads are in,
-      lds_barrier();                    // everyone's are, and everyone has read the stage that is filled next
-      // past the end the last block comes again, so that the loads in flight stay as many
-      if (ST > 2 || kb + 1 < part.kb_end) load(min(kb + ST - 1, part.kb_end - 1), stage == 0 ? ST - 1 : stage - 1);
-      step(stage);
-      stage = stage + 1 == ST ? 0 : stage + 1;
+    for (uint32_t first = part.kb0; first < part.kb_end; first += KS) {
+      wait_loads();   // this step's loads are in,
+      lds_barrier();  // everyone's are, and everyone has read the other stage
+      if (first + KS < part.kb_end) load(min(first + KS + share, last), stage ^ 1);
+      if (KS == 1 || first + share < part.kb_end) step(stage);
+      stage ^= 1;
     }
     if (PHASED && phase == 0) lds_barrier();
-    if (ST > 2) wait_loads<0>();  // nothing writes to LDS after the end
+  }
+
+  if (KS > 1) {  // the shares' sums meet in the first one's registers, in their order
+    f32x4(*sums)[MI * NI][kWaves][kWave] = reinterpret_cast<f32x4(*)[MI * NI][kWaves][kWave]>(&lds[0][0][0]);
+    static_assert((KS - 1) * sizeof sums[0] <= sizeof lds, "the sums fit the stages");
+    lds_barrier();
+    if (share > 0) {
+#pragma unroll
+      for (uint32_t i = 0; i < MI; ++i)
+#pragma unroll
+        for (uint32_t j = 0; j < NI; ++j) sums[share - 1][i * NI + j][wave][lane] = acc[i][j];
+    }
+    lds_barrier();
+    if (share > 0) return;
+#pragma unroll
+    for (uint32_t k = 0; k + 1 < KS; ++k)
+#pragma unroll
+      for (uint32_t i = 0; i < MI; ++i)
+#pragma unroll
+        for (uint32_t j = 0; j < NI; ++j) acc[i][j] += sums[k][i * NI + j][wave][lane];
   }
 
 #pragma unroll
@@ -546,7 +564,7 @@ hipError_t launch_rows(const Fp8Matmul &p, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <uint32_t BM, uint32_t BN, uint32_t WM, uint32_t WN, uint32_t ST, bool PHASED = false>
+template <uint32_t BM, uint32_t BN, uint32_t WM, uint32_t WN, uint32_t KS = 1, bool PHASED = false>
 hipError_t launch_tile(const Fp8Matmul &p, hipStream_t s) {
   Args a{p.a, p.b, p.sa, p.sb, p.d, p.m, p.n, p.kblocks, p.sa_stride, p.sb_stride, p.mode, p.offsets, p.groups, 0, 0};
   a.tiles_n = (p.n + BN - 1) / BN;
@@ -557,34 +575,37 @@ hipError_t launch_tile(const Fp8Matmul &p, hipStream_t s) {
   if (p.mode == kGroupedK) rows = static_cast<uint64_t>(a.tiles_m) * p.groups;
   const uint64_t blocks = rows * a.tiles_n;
   if (blocks >= (uint64_t{1} << 31)) return hipErrorInvalidConfiguration;
-  const dim3 grid(static_cast<uint32_t>(blocks)), threads(WM * WN * kWave);
+  const dim3 grid(static_cast<uint32_t>(blocks)), threads(WM * WN * KS * kWave);
   if (p.b_block_2d) {
-    if (p.out_fp32) hipLaunchKernelGGL((k_fp8_tile<BM, BN, WM, WN, ST, PHASED, false, true>), grid, threads, 0, s, a);
-    else hipLaunchKernelGGL((k_fp8_tile<BM, BN, WM, WN, ST, PHASED, false, false>), grid, threads, 0, s, a);
+    if (p.out_fp32) hipLaunchKernelGGL((k_fp8_tile<BM, BN, WM, WN, KS, PHASED, false, true>), grid, threads, 0, s, a);
+    else hipLaunchKernelGGL((k_fp8_tile<BM, BN, WM, WN, KS, PHASED, false, false>), grid, threads, 0, s, a);
   } else {
-    if (p.out_fp32) hipLaunchKernelGGL((k_fp8_tile<BM, BN, WM, WN, ST, PHASED, true, true>), grid, threads, 0, s, a);
-    else hipLaunchKernelGGL((k_fp8_tile<BM, BN, WM, WN, ST, PHASED, true, false>), grid, threads, 0, s, a);
+    if (p.out_fp32) hipLaunchKernelGGL((k_fp8_tile<BM, BN, WM, WN, KS, PHASED, true, true>), grid, threads, 0, s, a);
+    else hipLaunchKernelGGL((k_fp8_tile<BM, BN, WM, WN, KS, PHASED, true, false>), grid, threads, 0, s, a);
   }
   return hipGetLastError();
 }
 
 }  // namespace
 
-// Which kernel. Times in us, 128x128 tiles / 64x64 tiles / few rows:
-//   few rows (m up to 128, or 32 a group on average, by the buffer's rows):
-//     16 x 8192 x 5120        44 / 23 / 9.8      128 x 4096 x 4096   38 / 19 / 14.2
-//     64 groups, 1472 rows x 4096 x 2048  125 / 120 / 107
-//     against 256 x 4096 x 4096  39 / 20 / 28;   32 groups, 1504 rows x 2048 x 2048  35 / 37 / 46
-//   64x64 tiles up to 160 tiles of 128x128, where those leave CUs idle:
-//     777 x 1361 x 1999       24 / 17 / 24       512 x 4096 x 4096   40 / 29 / 52
-//     against 1024 x 4096 x 4096 (256 tiles)  46 / 56 / 103
-//   256x256 tiles where their rounds over 256 CUs, 3.2 us a step along k, take
-//   less than those of 128x128 tiles over 512 places, 1.8 us a step (times 128x128 / 256x256):
-//     8192 x 8192 x 5120      600 / 543          4096 x 4096 x 4096  132 / 117
-//     8 groups, 66552 rows x 4096 x 2048  1007 / 939
-//     against 3000 x 8192 x 5120  229 / 253;     16 groups, 34800 rows x 2048 x 4096  519 / 528
-//   By groups along k those are short, and 256x256 tiles lose (762 / 843 for
-//   32 groups, 4096 x 2048 x about 1100).
+// Which kernel. Times in us.
+//   Few rows, against 128x128 tiles: m up to 128, or 32 a group on average, by the buffer's rows:
+//     16 x 8192 x 5120        9.8 / 44           128 x 4096 x 4096  14.2 / 38
+//     64 groups, 1472 rows x 4096 x 2048  107 / 125
+//     but 256 x 4096 x 4096   28 / 39 (64x64 tiles 15);  32 groups, 1504 rows x 2048 x 2048  46 / 35
+//   Up to 160 tiles of 128x128 they leave CUs idle, and a wave that has its
+//   SIMD to itself takes 0.5 us a step, most of it waiting for its own last
+//   instruction. So up to 256 tiles of 64x64 (one a CU) those, with 16 waves in
+//   four shares of the blocks along k, against four waves and against 128x128:
+//     256 x 4096 x 4096       15.1 / 19.8 / 39   256 x 1024 x 8192  23 / 34
+//   and above that 64x128 tiles with 8 waves in two shares, against 64x64 with four waves:
+//     777 x 1361 x 1999       15.1 / 16.4        512 x 4096 x 4096  24 / 29
+//     but 1024 x 4096 x 2048 (256 tiles of 128x128)  26.6, and 128x128 24.7
+//   256x256 tiles, phased, where their rounds over 256 CUs, 3.2 us a step along
+//   k, take less than those of 128x128 tiles over 512 places, 1.8 us a step:
+//     8192 x 8192 x 5120      543 / 600          4096 x 4096 x 4096  117 / 132
+//     8 groups, 66552 rows x 4096 x 2048  939 / 1007;   32 weight gradients of 4096 x 2048  688 / 720
+//     but 3000 x 8192 x 5120  253 / 229;     16 groups, 34800 rows x 2048 x 4096  528 / 519
 hipError_t launch_fp8_matmul(const Fp8Matmul &p, hipStream_t s) {
   const bool few = p.mode == kDense ? p.m <= 128 : p.mode == kGroupedRows && p.m <= 32 * static_cast<uint64_t>(p.groups);
   if (few) {
@@ -600,10 +621,10 @@ hipError_t launch_fp8_matmul(const Fp8Matmul &p, hipStream_t s) {
     return rows * ((p.n + edge - 1) / edge) * (p.mode == kGroupedK ? p.groups : 1);
   };
   const uint64_t tiles = count(128);
-  if (tiles <= 160) return launch_tile<64, 64, 2, 2, 4>(p, s);
-  if (p.mode != kGroupedK && p.n % 256 == 0 && 64 * ((count(256) + 255) / 256) <= 35 * ((tiles + 511) / 512))
-    return launch_tile<256, 256, 2, 4, 2, true>(p, s);
-  return launch_tile<128, 128, 2, 2, 2>(p, s);
+  if (tiles <= 160) return count(64) <= 256 ? launch_tile<64, 64, 2, 2, 4>(p, s) : launch_tile<64, 128, 2, 2, 2>(p, s);
+  if (p.n % 256 == 0 && 64 * ((count(256) + 255) / 256) <= 35 * ((tiles + 511) / 512))
+    return launch_tile<256, 256, 2, 4, 1, true>(p, s);
+  return launch_tile<128, 128, 2, 2>(p, s);
 }
 
 }  // namespace nvfp4
