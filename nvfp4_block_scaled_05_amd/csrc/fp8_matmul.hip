@@ -545,7 +545,7 @@ __global__ __launch_bounds__(KS *kWave) void k_fp8_rows(Args p) {
   const uint32_t rows = part.m_end - part.m0;
   if (rows <= 16) rows_tile<KS, 1, 4, SBV, OUT32>(p, part, a, b, sa, sb, n0, red);
   else if (rows <= 32) rows_tile<KS, 2, 2, SBV, OUT32>(p, part, a, b, sa, sb, n0, red);
-  else rows_tile<KS, 4, 2, SBV, OUT32>(p, part, a, b, sa, sb, n0, red);
+  else rows_tile<KS, 4, 2, SBV, OUT32>(p, part, a, b, sa, sb, n0, red);  // a group's, above the average
 }
 
 template <uint32_t KS>
@@ -589,10 +589,10 @@ hipError_t launch_tile(const Fp8Matmul &p, hipStream_t s) {
 }  // namespace
 
 // Which kernel. Times in us.
-//   Few rows, against 128x128 tiles: m up to 128, or 32 a group on average, by the buffer's rows:
-//     16 x 8192 x 5120        9.8 / 44           128 x 4096 x 4096  14.2 / 38
-//     64 groups, 1472 rows x 4096 x 2048  107 / 125
-//     but 256 x 4096 x 4096   28 / 39 (64x64 tiles 15);  32 groups, 1504 rows x 2048 x 2048  46 / 35
+//   Few rows, against the 64x64 tiles below: m up to 32, or 24 a group on average, by the buffer's rows:
+//     16 x 8192 x 5120        9.8 / 16.2         32 x 4096 x 4096  10.1 / 12.9
+//     64 groups, 1472 rows x 4096 x 2048  107 / 120
+//     but 64 x 8192 x 5120    17.8 / 16.6;       32 groups, 992 rows x 2048 x 2048  35 / 34 in 128x128
 //   Up to 160 tiles of 128x128 they leave CUs idle, and a wave that has its
 //   SIMD to itself takes 0.5 us a step, most of it waiting for its own last
 //   instruction. So up to 256 tiles of 64x64 (one a CU) those, with 16 waves in
@@ -607,7 +607,7 @@ hipError_t launch_tile(const Fp8Matmul &p, hipStream_t s) {
 //     8 groups, 66552 rows x 4096 x 2048  939 / 1007;   32 weight gradients of 4096 x 2048  688 / 720
 //     but 3000 x 8192 x 5120  253 / 229;     16 groups, 34800 rows x 2048 x 4096  528 / 519
 hipError_t launch_fp8_matmul(const Fp8Matmul &p, hipStream_t s) {
-  const bool few = p.mode == kDense ? p.m <= 128 : p.mode == kGroupedRows && p.m <= 32 * static_cast<uint64_t>(p.groups);
+  const bool few = p.mode == kDense ? p.m <= 32 : p.mode == kGroupedRows && p.m <= 24 * static_cast<uint64_t>(p.groups);
   if (few) {
     // a wave's share is best at least the four blocks that it asks for at once
     if (p.kblocks >= 24) return launch_rows<8>(p, s);
