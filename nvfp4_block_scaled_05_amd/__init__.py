@@ -513,15 +513,14 @@ class Fp8Tensor:
         return nvfp4_fp8_t(self.data.data_ptr(), self.scales.data_ptr())
 
 
-def _is(t, dtype, shape, device) -> bool:
-    return (isinstance(t, torch.Tensor) and t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.is_contiguous()
-            and t.device == device)
-
-
+# These checks run on every call, most of which are short: each looks at the
+# tensor's attributes in place and builds its message only when it refuses.
 def _want(t, dtype, shape, device, what: str) -> None:
-    if not _is(t, dtype, shape, device):
-        got = f"{t.dtype} {tuple(t.shape)} on {t.device}" if isinstance(t, torch.Tensor) else type(t).__name__
-        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got {got}")
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
+            and t.is_contiguous()):
+        return
+    got = f"{t.dtype} {tuple(t.shape)} on {t.device}" if isinstance(t, torch.Tensor) else type(t).__name__
+    raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got {got}")
 
 
 def _on(x: torch.Tensor, what: str) -> torch.device:
@@ -542,9 +541,10 @@ def _current(device) -> int:
 
 def _want_plan(plan: ExpertPlan, device) -> None:
     a, b, o, c, i32 = plan.slot_rows, plan.row_slots, plan.offsets, plan.counts, torch.int32
-    for t in (a, b, o, c):
-        if t.dtype != i32 or t.device != device or not t.is_contiguous():
-            raise ValueError(f"a plan's tensors must be contiguous int32 tensors on {device}, got {t.dtype} on {t.device}")
+    if not (a.dtype is i32 and b.dtype is i32 and o.dtype is i32 and c.dtype is i32 and a.device == device
+            and b.device == device and o.device == device and c.device == device and a.is_contiguous()
+            and b.is_contiguous() and o.is_contiguous() and c.is_contiguous()):
+        raise ValueError(f"a plan's tensors must be contiguous int32 tensors on {device}")
     if a.dim() != 2 or b.dim() != 1 or c.dim() != 1 or o.dim() != 1 or o.shape[0] != c.shape[0] + 1:
         raise ValueError("a plan has slot_rows [tokens][topk], row_slots [rows], offsets [experts + 1] and counts [experts]")
 
@@ -570,8 +570,8 @@ def expert_sort(ids: torch.Tensor, experts: int, *, align: int = FP8_BLOCK, rows
              lib.nvfp4_expert_sort_workspace_bytes(tokens, topk, experts) // 4)
     slot_rows, row_slots, offsets, counts, ws = torch.split_with_sizes(ids.new_empty((sum(sizes),), dtype=torch.int32), sizes)
     slot_rows = slot_rows.view(tokens, topk)
-    _check(lib.nvfp4_expert_sort(_ptr(ids), ids.element_size(), tokens, topk, experts, align, rows, _ptr(slot_rows),
-                                 _ptr(row_slots), _ptr(offsets), _ptr(counts), _ptr(ws) if sizes[4] else None, _current(dev)))
+    _check(lib.nvfp4_expert_sort(ids.data_ptr(), ids.element_size(), tokens, topk, experts, align, rows, slot_rows.data_ptr(),
+                                 row_slots.data_ptr(), offsets.data_ptr(), counts.data_ptr(), _ptr(ws) if sizes[4] else None, _current(dev)))
     return ExpertPlan(slot_rows, row_slots, offsets, counts, align)
 
 
@@ -586,8 +586,8 @@ def expert_gather(x: torch.Tensor, plan: ExpertPlan, *, stream=None) -> torch.Te
         with _under(stream, dev):
             return expert_gather(x, plan)
     y = torch.empty((plan.rows, x.shape[1]), dtype=x.dtype, device=dev)
-    _check(load().nvfp4_expert_gather(_ptr(x), code, plan.tokens, plan.topk, x.shape[1], _ptr(plan.slot_rows),
-                                      _ptr(plan.row_slots), plan.rows, _ptr(y), _current(dev)))
+    _check(load().nvfp4_expert_gather(x.data_ptr(), code, plan.tokens, plan.topk, x.shape[1], plan.slot_rows.data_ptr(),
+                                      plan.row_slots.data_ptr(), plan.rows, y.data_ptr(), _current(dev)))
     return y
 
 
@@ -606,8 +606,8 @@ def expert_combine(y: torch.Tensor, plan: ExpertPlan, weights: Optional[torch.Te
         with _under(stream, dev):
             return expert_combine(y, plan, weights)
     out = torch.empty((plan.tokens, y.shape[1]), dtype=y.dtype, device=dev)
-    _check(load().nvfp4_expert_combine(_ptr(y), code, plan.tokens, plan.topk, y.shape[1], _ptr(plan.slot_rows), plan.rows,
-                                       _ptr(weights), _ptr(out), _current(dev)))
+    _check(load().nvfp4_expert_combine(y.data_ptr(), code, plan.tokens, plan.topk, y.shape[1], plan.slot_rows.data_ptr(), plan.rows,
+                                       _ptr(weights), out.data_ptr(), _current(dev)))
     return out
 
 
@@ -632,8 +632,8 @@ def expert_combine_grad(dout: torch.Tensor, y: torch.Tensor, plan: ExpertPlan, w
             return expert_combine_grad(dout, y, plan, weights)
     dy = torch.empty((plan.rows, cols), dtype=dout.dtype, device=dev)
     dw = torch.empty((plan.tokens, plan.topk), dtype=torch.float32, device=dev)
-    _check(load().nvfp4_expert_combine_grad(_ptr(dout), _ptr(y), code, plan.tokens, plan.topk, cols, _ptr(plan.slot_rows),
-                                            _ptr(plan.row_slots), plan.rows, _ptr(weights), _ptr(dy), _ptr(dw), _current(dev)))
+    _check(load().nvfp4_expert_combine_grad(dout.data_ptr(), y.data_ptr(), code, plan.tokens, plan.topk, cols, plan.slot_rows.data_ptr(),
+                                            plan.row_slots.data_ptr(), plan.rows, _ptr(weights), dy.data_ptr(), dw.data_ptr(), _current(dev)))
     return dy, dw
 
 
@@ -675,7 +675,7 @@ def fp8_quantize(x: torch.Tensor, *, rowwise=True, columnwise=False, block_2d=Fa
     row = empty(rows, cols) if rowwise else None
     col = empty(cols, rows) if columnwise else None
     r, c = row.as_c() if row is not None else None, col.as_c() if col is not None else None
-    _check(load().nvfp4_fp8_quantize(_ptr(x), code, batch, rows, cols, _ptr(slots), tokens, topk, int(block_2d), r, c, _current(dev)))
+    _check(load().nvfp4_fp8_quantize(x.data_ptr(), code, batch, rows, cols, _ptr(slots), tokens, topk, int(block_2d), r, c, _current(dev)))
     return row, col
 
 
@@ -683,9 +683,9 @@ def _want_fp8(q: Fp8Tensor, lead, n: int, k: int, block_2d: bool, device, what: 
     if q.n != n or q.k != k or bool(q.block_2d) != block_2d:
         raise ValueError(f"{what} must have {n} rows of {k} values in {'128x128' if block_2d else '1x128'} blocks, got "
                          f"{q.n} x {q.k}, block_2d={q.block_2d}")
-    kb = _blocks(k)
-    _want(q.data, torch.float8_e4m3fn, (*lead, n, kb * FP8_BLOCK), device, f"{what} data")
-    _want(q.scales, torch.float32, (*lead, kb, _blocks(n) if block_2d else n), device, f"{what} scales")
+    kb = (k + FP8_BLOCK - 1) // FP8_BLOCK
+    _want(q.data, torch.float8_e4m3fn, (*lead, n, kb * FP8_BLOCK), device, what)
+    _want(q.scales, torch.float32, (*lead, kb, (n + FP8_BLOCK - 1) // FP8_BLOCK if block_2d else n), device, what)
 
 
 def _out_code(dtype) -> int:
@@ -704,7 +704,7 @@ def fp8_matmul(a: Fp8Tensor, b: Fp8Tensor, *, out_dtype=torch.bfloat16, stream=N
         with _under(stream, dev):
             return fp8_matmul(a, b, out_dtype=out_dtype)
     d = torch.empty((a.n, b.n), dtype=out_dtype, device=dev)
-    _check(load().nvfp4_fp8_matmul(a.as_c(), b.as_c(), a.n, b.n, a.k, int(b.block_2d), _ptr(d), code, _current(dev)))
+    _check(load().nvfp4_fp8_matmul(a.as_c(), b.as_c(), a.n, b.n, a.k, int(b.block_2d), d.data_ptr(), code, _current(dev)))
     return d
 
 
@@ -721,8 +721,8 @@ def fp8_matmul_grouped(a: Fp8Tensor, b: Fp8Tensor, plan: ExpertPlan, *, out_dtyp
         with _under(stream, dev):
             return fp8_matmul_grouped(a, b, plan, out_dtype=out_dtype)
     d = torch.empty((plan.rows, b.n), dtype=out_dtype, device=dev)
-    _check(load().nvfp4_fp8_matmul_grouped(a.as_c(), b.as_c(), _ptr(plan.offsets), plan.experts, plan.rows, b.n, a.k,
-                                           _ptr(d), code, _current(dev)))
+    _check(load().nvfp4_fp8_matmul_grouped(a.as_c(), b.as_c(), plan.offsets.data_ptr(), plan.experts, plan.rows, b.n, a.k,
+                                           d.data_ptr(), code, _current(dev)))
     return d
 
 
@@ -741,6 +741,6 @@ def fp8_matmul_grouped_k(a: Fp8Tensor, b: Fp8Tensor, plan: ExpertPlan, *, out_dt
         with _under(stream, dev):
             return fp8_matmul_grouped_k(a, b, plan, out_dtype=out_dtype)
     d = torch.empty((plan.experts, a.n, b.n), dtype=out_dtype, device=dev)
-    _check(load().nvfp4_fp8_matmul_grouped_k(a.as_c(), b.as_c(), _ptr(plan.offsets), plan.experts, a.n, b.n, plan.rows,
-                                             _ptr(d), code, _current(dev)))
+    _check(load().nvfp4_fp8_matmul_grouped_k(a.as_c(), b.as_c(), plan.offsets.data_ptr(), plan.experts, a.n, b.n, plan.rows,
+                                             d.data_ptr(), code, _current(dev)))
     return d

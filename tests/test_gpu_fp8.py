@@ -178,6 +178,20 @@ def test_matmul_grouped_large(counts, align):
     assert not bool(d[off[-1]:].any())
 
 
+@pytest.mark.parametrize("m,n", [(1500, 1536), (700, 2048), (1300, 1000)])
+def test_matmul_grouped_k_large(m, n):
+    counts = [300, 0, 129, 1, 1100]
+    plan = plan_of(counts, 128, drop=9)
+    a = nv.fp8_quantize(rand((plan.tokens, m), torch.float32, m, spread=1.0), rowwise=False, columnwise=True, plan=plan)[1]
+    b = nv.fp8_quantize(rand((plan.tokens, n), torch.float32, n, spread=1.0), rowwise=False, columnwise=True, plan=plan)[1]
+    va, vb, off = on_device(a), on_device(b), H.i64(plan.offsets)
+    for out in (torch.float32, torch.bfloat16):
+        d = nv.fp8_matmul_grouped_k(a, b, plan, out_dtype=out)
+        for e in range(len(counts)):
+            r = slice(off[e], off[e + 1])
+            check_on_device(d[e], va[:, r], vb[:, r])
+
+
 @pytest.mark.parametrize("m", [1, 40, 600])
 def test_matmul_keeps_exact_sums_exact(m):
     # whole numbers below 2^24 in every partial sum, and scales that are powers of two
