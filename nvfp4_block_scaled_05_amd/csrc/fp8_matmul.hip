@@ -195,7 +195,8 @@ __device__ __forceinline__ Wide widen(u32x4 w) { return Wide{widen8(w.x, w.y), w
 // wait, then read and widen b, and leave the matrix cores idle together: 570
 // us. So the two waves of each SIMD run half a step apart. Waves 0 .. 3 (upper
 // half of the rows) begin a step at one barrier and pass the next one in the
-// middle of it, where waves 4 .. 7 begin theirs: 535 to 545 us (1.27 PFLOP/s).
+// middle of it, where waves 4 .. 7 begin theirs: 535 to 545 us, and 492 to 510 us
+// (1.35 to 1.40 PFLOP/s) with the instructions in groups, below.
 // What that needs of the two stages: each half of the waves loads its own rows
 // of a, at its own steps' beginnings; b is read at a step's beginning only, so
 // the stage that the lower half has read by the middle of its step k, which is
@@ -227,7 +228,9 @@ __global__ __launch_bounds__(WM *WN *KS *kWave) void k_fp8_tile(Args p) {
   constexpr uint32_t kLoadA = BM / 8 / kWaves, kLoadB = BN / 8 / kWaves;  // loads of 8 rows that a wave makes
   constexpr uint32_t kGroups = (BM + BN) / 64, kLoadS = (kGroups + kWaves - 1) / kWaves;
   static_assert((NI == 2 || NI % 4 == 0) && BM % (8 * kWaves) == 0 && BN % (8 * kWaves) == 0, "tile shape");
-  constexpr uint32_t kTurn = 3;  // of a phased wave's 8 row tiles, those before the barrier; 4: 2% slower, 2: 4%
+  // In groups of instructions (below) where the registers hold that.
+  constexpr bool kGrouped = NI == 4 && MI >= 4 && !(PHASED && SBV);
+  constexpr uint32_t kTurn = kGrouped ? 2 : 3;  // of a phased wave's 8 row tiles, those before the barrier; one more or less: 1 to 4% slower
   static_assert(!PHASED || (BM == 256 && BN == 256 && WM == 2 && WN == 4 && KS == 1), "phased shape");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[KS][2][(BM + BN) * kBlock];
   __shared__ __attribute__((aligned(16))) float scales[KS][2][BM + BN];
@@ -354,6 +357,87 @@ __global__ __launch_bounds__(WM *WN *KS *kWave) void k_fp8_tile(Args p) {
     }
   };
 
+  // The same with its instructions in an order of its own (the scheduler's has
+  // the matrix cores wait for the next fragment, and for sums of four dependent
+  // products; 8192 x 8192 x 5120 in 256x256 tiles took 535 us so, and takes
+  // 500): groups of two v_mfma of different tiles, each group with at most eight
+  // vector instructions beside it. Those widen half of the next fragment, or
+  // scale tiles whose products ended a group before.
+  auto step_in_groups = [&](uint32_t stage) {
+    if constexpr (kGrouped) {
+      const uint8_t *la = &lds[share][stage][wm * TM * kBlock], *lb = &lds[share][stage][(BM + wn * TN) * kBlock];
+      const float *ls = &scales[share][stage][wm * TM], *lsb = &scales[share][stage][BM + wn * TN];
+      const float sbu = SBV ? 1.0f : lsb[0];
+      f32x4 sbv[NI];
+      const uint32_t f = i16 & 7;
+      u32x4 lo = chunk_at(la, i16, q, f), hi = chunk_at(la, i16, q + 4, f);  // a's fragment, as loaded
+      float s = SBV ? ls[i16] : ls[i16] * sbu, s_next = 0.0f;
+      Wide b0[NI], b1[NI], a0 = widen(lo), a1;
+#pragma unroll
+      for (uint32_t j = 0; j < NI; ++j) {
+        const uint32_t r = (j / G) * 16 * G + (i16 / 4) * 4 * G + (j % G) * 4 + i16 % 4;
+        b0[j] = widen(chunk_at(lb, r, q, f));
+        b1[j] = widen(chunk_at(lb, r, q + 4, f));
+        if (SBV) sbv[j] = *reinterpret_cast<const f32x4 *>(lsb + (j / G) * 16 * G + q * 4 * G + (j % G) * 4);
+      }
+      f32x4 c[4];
+      auto product = [&](uint32_t j, const bf16x8 &x, const bf16x8 &y, bool first) {
+        c[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, y, first ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : c[j], 0, 0, 0);
+      };
+      auto scale = [&](uint32_t i, uint32_t j, float by) {
+#pragma unroll
+        for (uint32_t e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(c[j][e], SBV ? by * sbv[j][e] : by, acc[i][j][e]);
+      };
+      float s_last = 0.0f;
+#pragma unroll
+      for (uint32_t i = 0; i < MI; ++i) {
+        if (PHASED && i == kTurn) lds_barrier();
+        const bool more = i + 1 < MI;
+        product(0, b0[0].lo, a0.lo, true);
+        product(1, b0[1].lo, a0.lo, true);
+        a1.lo = widen8(hi.x, hi.y);
+        __builtin_amdgcn_sched_barrier(0);
+        product(0, b0[0].hi, a0.hi, false);
+        product(1, b0[1].hi, a0.hi, false);
+        a1.hi = widen8(hi.z, hi.w);
+        if (more) {
+          lo = chunk_at(la, (i + 1) * 16 + i16, q, f);
+          hi = chunk_at(la, (i + 1) * 16 + i16, q + 4, f);
+          s_next = ls[(i + 1) * 16 + i16];
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        product(0, b1[0].lo, a1.lo, false);
+        product(1, b1[1].lo, a1.lo, false);
+        if (i > 0) scale(i - 1, 2, s_last);
+        __builtin_amdgcn_sched_barrier(0);
+        product(0, b1[0].hi, a1.hi, false);
+        product(1, b1[1].hi, a1.hi, false);
+        if (i > 0) scale(i - 1, 3, s_last);
+        __builtin_amdgcn_sched_barrier(0);
+        product(2, b0[2].lo, a0.lo, true);
+        product(3, b0[3].lo, a0.lo, true);
+        __builtin_amdgcn_sched_barrier(0);
+        product(2, b0[2].hi, a0.hi, false);
+        product(3, b0[3].hi, a0.hi, false);
+        scale(i, 0, s);
+        __builtin_amdgcn_sched_barrier(0);
+        product(2, b1[2].lo, a1.lo, false);
+        product(3, b1[3].lo, a1.lo, false);
+        scale(i, 1, s);
+        if (more) a0.lo = widen8(lo.x, lo.y);
+        __builtin_amdgcn_sched_barrier(0);
+        product(2, b1[2].hi, a1.hi, false);
+        product(3, b1[3].hi, a1.hi, false);
+        if (more) a0.hi = widen8(lo.z, lo.w);
+        s_last = s;
+        s = SBV ? s_next : s_next * sbu;
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      scale(MI - 1, 2, s_last);
+      scale(MI - 1, 3, s_last);
+    }
+  };
+
   if (!part.zero && part.kb0 < part.kb_end) {
     // (a share without a block in the last round loads the last one and leaves it)
     const uint32_t last = part.kb_end - 1;
@@ -364,7 +448,10 @@ __global__ __launch_bounds__(WM *WN *KS *kWave) void k_fp8_tile(Args p) {
       wait_loads();   // this step's loads are in,
       lds_barrier();  // everyone's are, and everyone has read the other stage
       if (first + KS < part.kb_end) load(min(first + KS + share, last), stage ^ 1);
-      if (KS == 1 || first + share < part.kb_end) step(stage);
+      if (KS == 1 || first + share < part.kb_end) {
+        if (kGrouped) step_in_groups(stage);
+        else step(stage);
+      }
       stage ^= 1;
     }
     if (PHASED && phase == 0) lds_barrier();
@@ -601,11 +688,11 @@ hipError_t launch_tile(const Fp8Matmul &p, hipStream_t s) {
 //   and above that 64x128 tiles with 8 waves in two shares, against 64x64 with four waves:
 //     777 x 1361 x 1999       15.1 / 16.4        512 x 4096 x 4096  24 / 29
 //     but 1024 x 4096 x 2048 (256 tiles of 128x128)  26.6, and 128x128 24.7
-//   256x256 tiles, phased, where their rounds over 256 CUs, 3.2 us a step along
+//   256x256 tiles, phased, where their rounds over 256 CUs, 3.1 us a step along
 //   k, take less than those of 128x128 tiles over 512 places, 1.8 us a step:
-//     8192 x 8192 x 5120      543 / 600          4096 x 4096 x 4096  117 / 132
+//     8192 x 8192 x 5120      500 / 580          4096 x 4096 x 4096  117 / 132
 //     8 groups, 66552 rows x 4096 x 2048  939 / 1007;   32 weight gradients of 4096 x 2048  688 / 720
-//     but 3000 x 8192 x 5120  253 / 229;     16 groups, 34800 rows x 2048 x 4096  528 / 519
+//     but 3000 x 8192 x 5120  253 / 229
 hipError_t launch_fp8_matmul(const Fp8Matmul &p, hipStream_t s) {
   const bool few = p.mode == kDense ? p.m <= 32 : p.mode == kGroupedRows && p.m <= 24 * static_cast<uint64_t>(p.groups);
   if (few) {
@@ -622,7 +709,7 @@ hipError_t launch_fp8_matmul(const Fp8Matmul &p, hipStream_t s) {
   };
   const uint64_t tiles = count(128);
   if (tiles <= 160) return count(64) <= 256 ? launch_tile<64, 64, 2, 2, 4>(p, s) : launch_tile<64, 128, 2, 2, 2>(p, s);
-  if (p.n % 256 == 0 && 64 * ((count(256) + 255) / 256) <= 35 * ((tiles + 511) / 512))
+  if (p.n % 256 == 0 && 64 * ((count(256) + 255) / 256) <= 37 * ((tiles + 511) / 512))
     return launch_tile<256, 256, 2, 4, 1, true>(p, s);
   return launch_tile<128, 128, 2, 2>(p, s);
 }
