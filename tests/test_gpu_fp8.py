@@ -305,6 +305,32 @@ def test_weights_past_32_bits():
         H.close(d[first:first + rows], H.f64(va @ vb.t()), H.f64(bound))
 
 
+def test_quantize_past_32_bits():
+    # more than 2^32 input elements and 2^32 bytes in each output
+    rows, cols = 140032, 32768
+    block = rand((256, cols), torch.bfloat16, 7)
+    x = block.repeat(rows // 256, 1)
+    row, col = nv.fp8_quantize(x, columnwise=True)
+    assert row.data.numel() > 1 << 32 and col.data.numel() > 1 << 32
+    want_row, want_col = nv.fp8_quantize(block, columnwise=True)
+    for first in (0, rows // 512 * 256, rows - 256):
+        assert torch.equal(row.data[first:first + 256].view(torch.uint8), want_row.data.view(torch.uint8))
+        assert torch.equal(row.scales[:, first:first + 256], want_row.scales)
+        assert torch.equal(col.data[:, first:first + 256].view(torch.uint8), want_col.data.view(torch.uint8))
+        assert torch.equal(col.scales[first // 128:first // 128 + 2], want_col.scales)
+
+
+@pytest.mark.parametrize("n,out", [(32768, torch.bfloat16), (32700, torch.float32)])
+def test_output_past_32_bits(n, out):
+    m, k = 70000, 128
+    a, b = operand(m, k, False, 1), operand(n, k, True, 2)
+    d = nv.fp8_matmul(a, b, out_dtype=out)
+    assert d.numel() * d.element_size() > 1 << 32
+    va, vb = on_device(a), on_device(b)
+    for first in (0, 35000, m - 300):
+        check_on_device(d[first:first + 300], va[first:first + 300], vb)
+
+
 def test_products_in_a_graph_and_on_another_stream():
     plan = plan_of([40, 0, 200, 30], 128)
     x = rand((plan.tokens, 256), torch.bfloat16, 1)
