@@ -309,6 +309,7 @@ __global__ __launch_bounds__(WM *WN *KS *kWave) void k_fp8_tile(Args p) {
   };
 
   const uint32_t wm = PHASED ? phase : wave % WM, wn = PHASED ? quarter : wave / WM;
+  const bool active = m0 + wm * TM < part.m_end;  // a phased tile's lower half may have no rows: its waves then only load and wait
   const uint32_t i16 = lane % 16, q = lane / 16;
   f32x4 acc[MI][NI];
 #pragma unroll
@@ -449,7 +450,8 @@ __global__ __launch_bounds__(WM *WN *KS *kWave) void k_fp8_tile(Args p) {
       lds_barrier();  // everyone's are, and everyone has read the other stage
       if (first + KS < part.kb_end) load(min(first + KS + share, last), stage ^ 1);
       if (KS == 1 || first + share < part.kb_end) {
-        if (kGrouped) step_in_groups(stage);
+        if (PHASED && !active) lds_barrier();
+        else if (kGrouped) step_in_groups(stage);
         else step(stage);
       }
       stage ^= 1;
