@@ -465,10 +465,13 @@ uint64_t nvfp4_fp8_pitch(int64_t k);
  * one read; row or col may be NULL, not both. block_2d 0: 1x128 blocks along
  * each orientation's rows; 1: 128x128 blocks, whose scales both orientations
  * share (transposed).
- * Per block: s = fl(max|v| / 448), e = fl(1 / s) (0 when s == 0, at most
- * FLT_MAX), code = E4M3(fl(v * e)), nearest even, saturating at 448. The
- * rows and columns that a block lacks count as zeros. A block with a NaN has
- * a NaN scale, one with an infinity an infinite one.
+ * Per block: s = fl(max|v| / 448), e = fl(1 / s) (at most FLT_MAX; 0 unless s
+ * > 0), code = E4M3(fl(v * e)), nearest even, at most 448. (Where s < 2^-128,
+ * max|v| below some 1.3e-36, FLT_MAX cuts e short and the block decodes to less
+ * than it held.) The rows and columns that a block lacks count as zeros. A
+ * block with a NaN has a NaN scale, one with an infinity an infinite one; the
+ * codes of such a block are NaN where the value is not finite and 0 elsewhere,
+ * so that all of it decodes to NaN.
  * With row_slots (int32 [rows], batch 1): x is [tokens][cols] and row r of the
  * matrix is x[row_slots[r] / topk], zeros where row_slots[r] is not a slot
  * (0 .. tokens * topk - 1): nvfp4_expert_gather and this call in one. Without

@@ -2,8 +2,16 @@
 // for each block of 128 (1x128 along a row, or 128x128), in the row-wise and
 // the column-wise (transposed) orientation from one read of the input.
 //
-//   s = fl(max|v| / 448)   e = fl(1 / s), 0 when s == 0, at most FLT_MAX
-//   code = E4M3(clamp(fl(v * e), -448, 448)), nearest even
+//   s = fl(max|v| / 448)   e = fl(1 / s), at most FLT_MAX; 0 unless s > 0
+//   code = E4M3(fl(v * e)), nearest even
+//
+// No value needs a clamp: |v| <= 448 s (1 + 2^-22) and e <= (1 / s) (1 + 2^-24) for
+// s from 2^-128 up (below that FLT_MAX cuts e short, and |v e| < 448), so |v e| exceeds
+// 448 by 2^-21 of it at most, and what is below 464 rounds to 448. A block with an infinity
+// or a NaN has s infinite or NaN, hence e 0: its finite values get zero codes, the
+// others 0 * inf or 0 * NaN, which converts to the NaN code, so that all of it
+// decodes to NaN. (A clamp by v_med3_f32 would make -448 of those NaN, and -inf of
+// an infinity of either sign.)
 //
 // One workgroup per 128x128 tile, in registers: thread t holds the 8x8 patch
 // at rows 8 (t / 16), columns 8 (t % 16), so that 16 lanes read 256
@@ -79,8 +87,6 @@ __device__ __forceinline__ Scale block_scale_fp8(uint32_t amax_bits) {
   r.e = r.s > 0.0f ? fminf(1.0f / r.s, kFltMax) : 0.0f;
   return r;
 }
-
-__device__ __forceinline__ float scaled(float v, float e) { return __builtin_amdgcn_fmed3f(v * e, -kE4m3Max, kE4m3Max); }
 
 __device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) {
   int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
@@ -257,8 +263,8 @@ __global__ __launch_bounds__(kThreads) void k_fp8_quantize(Args a) {
       const uint32_t r = r0 + 8 * rg + p;
       const float e = BLOCK_2D ? tile_scale.e : row_mult[8 * rg + p];
       u32x2 w;
-      w.x = pack4(scaled(v.get(p, 0), e), scaled(v.get(p, 1), e), scaled(v.get(p, 2), e), scaled(v.get(p, 3), e));
-      w.y = pack4(scaled(v.get(p, 4), e), scaled(v.get(p, 5), e), scaled(v.get(p, 6), e), scaled(v.get(p, 7), e));
+      w.x = pack4(v.get(p, 0) * e, v.get(p, 1) * e, v.get(p, 2) * e, v.get(p, 3) * e);
+      w.y = pack4(v.get(p, 4) * e, v.get(p, 5) * e, v.get(p, 6) * e, v.get(p, 7) * e);
       if (r < a.rows) put<STREAM>(reinterpret_cast<u32x2 *>(dst + static_cast<uint64_t>(r) * (static_cast<uint64_t>(a.col_tiles) * kTile)), w);
     }
   }
@@ -270,8 +276,8 @@ __global__ __launch_bounds__(kThreads) void k_fp8_quantize(Args a) {
     for (int q = 0; q < 8; ++q) {
       const float e = BLOCK_2D ? tile_scale.e : col_mult[8 * cg + q];
       u32x2 w;
-      w.x = pack4(scaled(v.get(0, q), e), scaled(v.get(1, q), e), scaled(v.get(2, q), e), scaled(v.get(3, q), e));
-      w.y = pack4(scaled(v.get(4, q), e), scaled(v.get(5, q), e), scaled(v.get(6, q), e), scaled(v.get(7, q), e));
+      w.x = pack4(v.get(0, q) * e, v.get(1, q) * e, v.get(2, q) * e, v.get(3, q) * e);
+      w.y = pack4(v.get(4, q) * e, v.get(5, q) * e, v.get(6, q) * e, v.get(7, q) * e);
       turned[8 * cg + q][rg ^ cg] = w;
     }
     __syncthreads();
