@@ -487,7 +487,9 @@ nvfp4_status_t nvfp4_fp8_quantize(const void *x, nvfp4_dtype_t dtype, int64_t ba
  * d_dtype, 16-byte aligned. Any m, n; k < 2^23; k = 0 gives zeros. With the
  * orientations of nvfp4_fp8_quantize: y = x w^T takes x row-wise and w
  * row-wise, dx = dy w takes dy row-wise and w column-wise, dw = dy^T x takes
- * both column-wise.
+ * both column-wise. Scales may be any FP32 numbers, also where the product of
+ * two leaves FP32's range; but tiles that meet such a pair (b in 1x128 blocks: a
+ * scale of a outside 2^-108 .. 2^103) take some ten times as long.
  */
 nvfp4_status_t nvfp4_fp8_matmul(const nvfp4_fp8_t *a, const nvfp4_fp8_t *b, int64_t m, int64_t n, int64_t k,
                                 uint32_t b_block_2d, void *d, nvfp4_dtype_t d_dtype, void *stream);

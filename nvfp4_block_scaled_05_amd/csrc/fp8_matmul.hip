@@ -15,7 +15,17 @@
 // instruction makes two, beside the matrix core's work), and four
 // v_mfma_f32_16x16x32_bf16 sum a block's products of a 16x16 tile. The sum
 // then enters the accumulators, binary32 as well, by one fused multiply-add
-// with the block's scale; d is rounded once at the end.
+// with the product of the block's two scales; d is rounded once at the end.
+//
+// That product may leave binary32's range where the term does not (1e-25 * 1e-25 *
+// 2e7), or where the sum is 0. (b in 1x128 blocks: the sum times a's scale enters by
+// a multiply-add with b's, and that first product may.) The tile kernels therefore
+// look at the scales that they use (near()), and where that could be, the wave
+// computes its part of the tile again, by add_far(), which multiplies mantissas and
+// adds exponents. Looking costs 2 to 4% up to 512 rows and 1 to 2% above (512 x 4096 x
+// 4096 22.3 -> 22.7 us, 8192 x 8192 x 5120 498 -> 503); a product whose every tile is
+// computed again takes ten times as long. The few-row kernel, which has time beside
+// its loads, always takes add_far().
 #include "codec.h"
 #include "launch.h"
 
@@ -143,6 +153,23 @@ __device__ __forceinline__ void store(void *d, uint64_t row, uint32_t j, uint32_
   }
 }
 
+template <bool OUT32>
+__device__ __forceinline__ void store4(void *d, uint64_t row, uint32_t j, uint32_t n, f32x4 v) {
+  if (j + 4 <= n) {
+    if (OUT32) {
+      *reinterpret_cast<u32x4_any *>(static_cast<float *>(d) + row + j) =
+          u32x4_any{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+    } else {
+      typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
+      *reinterpret_cast<u32x2_any *>(static_cast<uint16_t *>(d) + row + j) = u32x2_any{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+    }
+  } else {
+#pragma unroll
+    for (uint32_t q = 0; q < 4; ++q)
+      if (j + q < n) store1<OUT32>(d, row + j + q, v[q]);
+  }
+}
+
 // Loads straight to LDS, 16 bytes or 4 a lane: lane l's go to `to` + 16 l (4 l),
 // from `from` + `offset`. Written out, since the compiler waits for every
 // such load before the next LDS read, whichever stage it reads. They have no
@@ -174,6 +201,35 @@ __device__ __forceinline__ bf16x8 widen8(uint32_t x, uint32_t y) {
   return bf16x8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
 }
 __device__ __forceinline__ Wide widen(u32x4 w) { return Wide{widen8(w.x, w.y), widen8(w.z, w.w)}; }
+
+// A block's sums of 128 products of a 16x16 tile.
+__device__ __forceinline__ f32x4 block_sum(const Wide &b0, const Wide &b1, const Wide &a0, const Wide &a1) {
+  f32x4 c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b0.lo, a0.lo, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
+  c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b0.hi, a0.hi, c, 0, 0, 0);
+  c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b1.lo, a1.lo, c, 0, 0, 0);
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(b1.hi, a1.hi, c, 0, 0, 0);
+}
+
+// Whether a block's sum can be scaled the short way: with 128x128 blocks of b,
+// where sa * sb is 0 for a 0 scale or a normal number; with 1x128 blocks, where
+// c * sa is, for any sum c other than 0: 2^-18 to 2^24.7.
+template <bool SBV>
+__device__ __forceinline__ bool near(float sa, float sb) {
+  constexpr int kNormal = 0x108;  // of either sign
+  if (!SBV) return __builtin_amdgcn_classf(sa * sb, kNormal) || sa == 0.0f || sb == 0.0f;
+  return fabsf(sa) < 0x1p103f && (fabsf(sa) >= 0x1p-108f || sa == 0.0f);
+}
+
+// acc + c * sa * sb for scales of any size: the term is what binary32 holds of it,
+// an infinity only where it is too large.
+__device__ __forceinline__ f32x4 add_far(f32x4 acc, f32x4 c, float sa, f32x4 sb) {
+  const float ma = __builtin_amdgcn_frexp_mantf(sa);
+  const int ea = __builtin_amdgcn_frexp_expf(sa);
+#pragma unroll
+  for (uint32_t e = 0; e < 4; ++e)
+    acc[e] += __builtin_amdgcn_ldexpf(c[e] * (ma * __builtin_amdgcn_frexp_mantf(sb[e])), ea + __builtin_amdgcn_frexp_expf(sb[e]));
+  return acc;
+}
 
 // ---------------------------------------------------------------------------
 // Tiles of BM x BN, WM x WN waves, each wave (BM / WM) x (BN / WN). A step
@@ -224,16 +280,16 @@ __global__ __launch_bounds__(WM *WN *KS *kWave) void k_fp8_tile(Args p) {
   constexpr uint32_t kWaves = WM * WN;
   constexpr uint32_t TM = BM / WM, TN = BN / WN, MI = TM / 16, NI = TN / 16;
   constexpr uint32_t G = OUT32 ? 1 : 2, NG = NI / G;  // 16-row tiles of b that share 16 G rows
-  constexpr uint32_t NS = NI < 4 ? 1 : NI / 4;        // scales of b in 128x128 blocks, for 64 columns each
   constexpr uint32_t kLoadA = BM / 8 / kWaves, kLoadB = BN / 8 / kWaves;  // loads of 8 rows that a wave makes
   constexpr uint32_t kGroups = (BM + BN) / 64, kLoadS = (kGroups + kWaves - 1) / kWaves;
-  static_assert((NI == 2 || NI % 4 == 0) && BM % (8 * kWaves) == 0 && BN % (8 * kWaves) == 0, "tile shape");
+  static_assert((NI == 2 || NI == 4) && BM % (8 * kWaves) == 0 && BN % (8 * kWaves) == 0, "tile shape");
   // In groups of instructions (below) where the registers hold that.
   constexpr bool kGrouped = NI == 4 && MI >= 4 && !(PHASED && SBV);
   constexpr uint32_t kTurn = kGrouped ? 2 : 3;  // of a phased wave's 8 row tiles, those before the barrier; one more or less: 1 to 4% slower
   static_assert(!PHASED || (BM == 256 && BN == 256 && WM == 2 && WN == 4 && KS == 1), "phased shape");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[KS][2][(BM + BN) * kBlock];
   __shared__ __attribute__((aligned(16))) float scales[KS][2][BM + BN];
+  __shared__ bool far_waves[KS > 1 ? kWaves : 1];  // of the first share's waves, those whose other shares met scales that are not near
 
   const uint32_t lane = threadIdx.x % kWave, any_wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const uint32_t wave = any_wave % kWaves, share = any_wave / kWaves;  // of the waves that share a tile's blocks along k
@@ -323,14 +379,27 @@ __global__ __launch_bounds__(WM *WN *KS *kWave) void k_fp8_tile(Args p) {
     return *reinterpret_cast<const u32x4 *>(base + r * kBlock + ((g ^ f) << 4));
   };
 
+  // The lanes that met scales that are not near(): with any, the wave's sums do not count.
+  uint64_t far = 0;
+  const uint32_t look = PHASED ? 0 : lane % TM;
+  auto look_at_scales = [&](const float *ls, float sbu) {
+    uint32_t l = look;
+    if (PHASED) {  // the lane's number anew, so that it holds no register through the steps
+      uint32_t all = ~0u;
+      asm volatile("" : "+s"(all));
+      l = __builtin_amdgcn_mbcnt_hi(all, __builtin_amdgcn_mbcnt_lo(all, 0));
+    }
+    bool ok = true;
+#pragma unroll
+    for (uint32_t i = 0; i < TM; i += kWave) ok = ok & near<SBV>(ls[i + l], sbu);
+    far |= __ballot(!ok);
+  };
+
   auto step = [&](uint32_t stage) {
     const uint8_t *la = &lds[share][stage][wm * TM * kBlock], *lb = &lds[share][stage][(BM + wn * TN) * kBlock];
     const float *ls = &scales[share][stage][wm * TM], *lsb = &scales[share][stage][BM + wn * TN];
-    float sbu[NS];
-    if (!SBV) {
-#pragma unroll
-      for (uint32_t g = 0; g < NS; ++g) sbu[g] = lsb[64 * g];
-    }
+    const float sbu = SBV ? 1.0f : lsb[0];  // its columns are in one 128x128 block of b
+    look_at_scales(ls, sbu);
     Wide b0[NI], b1[NI];
     f32x4 sbv[NI];
 #pragma unroll
@@ -348,12 +417,9 @@ __global__ __launch_bounds__(WM *WN *KS *kWave) void k_fp8_tile(Args p) {
       const float s = ls[i * 16 + i16];
 #pragma unroll
       for (uint32_t j = 0; j < NI; ++j) {
-        f32x4 c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b0[j].lo, a0.lo, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
-        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b0[j].hi, a0.hi, c, 0, 0, 0);
-        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b1[j].lo, a1.lo, c, 0, 0, 0);
-        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b1[j].hi, a1.hi, c, 0, 0, 0);
+        const f32x4 c = block_sum(b0[j], b1[j], a0, a1);
 #pragma unroll
-        for (uint32_t e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(c[e], SBV ? s * sbv[j][e] : s * sbu[j / 4], acc[i][j][e]);
+        for (uint32_t e = 0; e < 4; ++e) acc[i][j][e] = SBV ? __builtin_fmaf(c[e] * s, sbv[j][e], acc[i][j][e]) : __builtin_fmaf(c[e], s * sbu, acc[i][j][e]);
       }
     }
   };
@@ -369,6 +435,7 @@ __global__ __launch_bounds__(WM *WN *KS *kWave) void k_fp8_tile(Args p) {
       const uint8_t *la = &lds[share][stage][wm * TM * kBlock], *lb = &lds[share][stage][(BM + wn * TN) * kBlock];
       const float *ls = &scales[share][stage][wm * TM], *lsb = &scales[share][stage][BM + wn * TN];
       const float sbu = SBV ? 1.0f : lsb[0];
+      look_at_scales(ls, sbu);
       f32x4 sbv[NI];
       const uint32_t f = i16 & 7;
       u32x4 lo = chunk_at(la, i16, q, f), hi = chunk_at(la, i16, q + 4, f);  // a's fragment, as loaded
@@ -387,7 +454,7 @@ __global__ __launch_bounds__(WM *WN *KS *kWave) void k_fp8_tile(Args p) {
       };
       auto scale = [&](uint32_t i, uint32_t j, float by) {
 #pragma unroll
-        for (uint32_t e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(c[j][e], SBV ? by * sbv[j][e] : by, acc[i][j][e]);
+        for (uint32_t e = 0; e < 4; ++e) acc[i][j][e] = SBV ? __builtin_fmaf(c[j][e] * by, sbv[j][e], acc[i][j][e]) : __builtin_fmaf(c[j][e], by, acc[i][j][e]);
       };
       float s_last = 0.0f;
 #pragma unroll
@@ -439,6 +506,7 @@ __global__ __launch_bounds__(WM *WN *KS *kWave) void k_fp8_tile(Args p) {
     }
   };
 
+  if (KS > 1 && threadIdx.x < kWaves) far_waves[threadIdx.x] = false;  // read and written past a barrier
   if (!part.zero && part.kb0 < part.kb_end) {
     // (a share without a block in the last round loads the last one and leaves it)
     const uint32_t last = part.kb_end - 1;
@@ -459,11 +527,37 @@ __global__ __launch_bounds__(WM *WN *KS *kWave) void k_fp8_tile(Args p) {
     if (PHASED && phase == 0) lds_barrier();
   }
 
+  // The wave's part of the tile from memory, 16x16 sums at a time, all blocks along k: add_far()'s way.
+  auto far_tile = [&] {
+#pragma unroll 1
+    for (uint32_t i = 0; i < MI; ++i) {
+      const uint32_t row = wm * TM + i * 16 + i16, ra = min(row, part.m_end - 1 - m0);
+#pragma unroll 1
+      for (uint32_t j = 0; j < NI; ++j) {
+        const uint32_t col = wn * TN + j * 16, rb = min(col + i16, p.n - 1 - n0);
+        f32x4 v{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 2
+        for (uint32_t kb = part.kb0; kb < part.kb_end; ++kb) {
+          const uint64_t at = static_cast<uint64_t>(kb) * kBlock + 16 * q;
+          const u32x4 *pa = reinterpret_cast<const u32x4 *>(a + ra * pitch + at), *pb = reinterpret_cast<const u32x4 *>(b + rb * pitch + at);
+          const float *ps = sb + static_cast<uint64_t>(kb) * p.sb_stride;
+          f32x4 s;
+#pragma unroll
+          for (uint32_t e = 0; e < 4; ++e) s[e] = ps[SBV ? min(col + 4 * q + e, p.n - 1 - n0) : min((n0 + col) / kBlock, p.sb_stride - 1)];
+          v = add_far(v, block_sum(widen(pb[0]), widen(pb[4]), widen(pa[0]), widen(pa[4])), sa[static_cast<uint64_t>(kb) * p.sa_stride + ra], s);
+        }
+        const uint32_t m = m0 + row;
+        if (m < part.m_end) store4<OUT32>(p.d, d_base + static_cast<uint64_t>(m) * p.n, n0 + col + 4 * q, p.n, v);
+      }
+    }
+  };
+
   if (KS > 1) {  // the shares' sums meet in the first one's registers, in their order
     f32x4(*sums)[MI * NI][kWaves][kWave] = reinterpret_cast<f32x4(*)[MI * NI][kWaves][kWave]>(&lds[0][0][0]);
     static_assert((KS - 1) * sizeof sums[0] <= sizeof lds, "the sums fit the stages");
     lds_barrier();
     if (share > 0) {
+      if (far != 0) far_waves[wave] = true;
 #pragma unroll
       for (uint32_t i = 0; i < MI; ++i)
 #pragma unroll
@@ -471,6 +565,7 @@ __global__ __launch_bounds__(WM *WN *KS *kWave) void k_fp8_tile(Args p) {
     }
     lds_barrier();
     if (share > 0) return;
+    if (far_waves[wave]) far = 1;
 #pragma unroll
     for (uint32_t k = 0; k + 1 < KS; ++k)
 #pragma unroll
@@ -479,6 +574,10 @@ __global__ __launch_bounds__(WM *WN *KS *kWave) void k_fp8_tile(Args p) {
         for (uint32_t j = 0; j < NI; ++j) acc[i][j] += sums[k][i * NI + j][wave][lane];
   }
 
+  if (far != 0) {
+    far_tile();
+    return;
+  }
 #pragma unroll
   for (uint32_t i = 0; i < MI; ++i) {
     const uint32_t m = m0 + wm * TM + i * 16 + i16;
@@ -502,23 +601,6 @@ __global__ __launch_bounds__(WM *WN *KS *kWave) void k_fp8_tile(Args p) {
 // each row of b is read once and by one wave, so LDS would only add a step.
 // ---------------------------------------------------------------------------
 constexpr uint32_t kRowsM = 64, kRowsN = 32;
-
-template <bool OUT32>
-__device__ __forceinline__ void store4(void *d, uint64_t row, uint32_t j, uint32_t n, f32x4 v) {
-  if (j + 4 <= n) {
-    if (OUT32) {
-      *reinterpret_cast<u32x4_any *>(static_cast<float *>(d) + row + j) =
-          u32x4_any{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
-    } else {
-      typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
-      *reinterpret_cast<u32x2_any *>(static_cast<uint16_t *>(d) + row + j) = u32x2_any{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
-    }
-  } else {
-#pragma unroll
-    for (uint32_t q = 0; q < 4; ++q)
-      if (j + q < n) store1<OUT32>(d, row + j + q, v[q]);
-  }
-}
 
 template <uint32_t KS, uint32_t MT, uint32_t U, bool SBV, bool OUT32>
 __device__ __forceinline__ void rows_tile(const Args &p, const Part &part, const uint8_t *a, const uint8_t *b, const float *sa,
@@ -588,12 +670,9 @@ __device__ __forceinline__ void rows_tile(const Args &p, const Part &part, const
         const Wide a0 = widen(wa[u][i][0]), a1 = widen(wa[u][i][1]);
 #pragma unroll
         for (uint32_t t = 0; t < 2; ++t) {
-          f32x4 c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b0[t].lo, a0.lo, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
-          c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b0[t].hi, a0.hi, c, 0, 0, 0);
-          c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b1[t].lo, a1.lo, c, 0, 0, 0);
-          c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b1[t].hi, a1.hi, c, 0, 0, 0);
-#pragma unroll
-          for (uint32_t e = 0; e < 4; ++e) acc[i][t][e] = __builtin_fmaf(c[e], fa[u][i] * fb[u][SBV ? t : 0][SBV ? e : 0], acc[i][t][e]);
+          const float *f = fb[u][SBV ? t : 0];
+          acc[i][t] = add_far(acc[i][t], block_sum(b0[t], b1[t], a0, a1), fa[u][i],
+                              SBV ? f32x4{f[0], f[1], f[2], f[3]} : f32x4{f[0], f[0], f[0], f[0]});
         }
       }
     }
