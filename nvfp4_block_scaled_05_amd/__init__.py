@@ -530,8 +530,13 @@ def _on(x: torch.Tensor, what: str) -> torch.device:
 
 
 def _under(stream, device):
-    """The context of a call that was given a stream of its own."""
-    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device))
+    """The context of a call that was given a stream of its own: torch's, an
+    object with its handle in cuda_stream, or the handle."""
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(getattr(stream, "cuda_stream", stream))
+        # ExternalStream takes 0, the default stream's handle, for none given and makes a new stream
+        stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
 
 
 def _current(device) -> int:
