@@ -14,6 +14,7 @@ Tensors passed in are torch CUDA tensors (on ROCm, HIP devices):
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
 import os
@@ -194,6 +195,16 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _under(stream, device):
+    """The context of a call that was given a stream of its own: torch's, an
+    object with its handle in cuda_stream, or the handle."""
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(getattr(stream, "cuda_stream", stream))
+        # ExternalStream takes 0, the default stream's handle, for none given and makes a new stream
+        stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
 def _shape2d(x: torch.Tensor):
     if x.dim() != 2 or not x.is_contiguous() or not x.is_cuda:
         raise ValueError("x must be a contiguous 2-D CUDA tensor")
@@ -339,11 +350,9 @@ def quantize_grouped(x: torch.Tensor, group_rows, *, rowwise=True, columnwise=Tr
     col = orient(G) if columnwise else None
     ws = None
     if use_workspace and not cfg.workspace and cfg.compute_amax and not cfg.row_scaled:
-        ws = empty_workspace(dev)
+        ws = _clear_workspace(dev, stream)
         cfg = nvfp4_config_t.from_buffer_copy(cfg)
         cfg.workspace = ws.data_ptr()
-        if stream is not None:
-            ws.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
     nvfp4_quantize_grouped(x, group_rows, row, col, cfg, stream)
     del ws
     return row, col
@@ -396,6 +405,13 @@ def empty_workspace(device) -> torch.Tensor:
     return torch.zeros((nvfp4_workspace_bytes(),), dtype=torch.uint8, device=device)
 
 
+def _clear_workspace(device, stream) -> torch.Tensor:
+    """An empty_workspace() that is allocated and cleared on `stream`, so that
+    the call on it comes after that and its memory is not used again before."""
+    with contextlib.nullcontext() if stream is None else _under(stream, device):
+        return empty_workspace(device)
+
+
 _workspaces = {}
 
 
@@ -408,14 +424,12 @@ def stream_workspace(device, stream=None) -> torch.Tensor:
         dev = torch.device(dev.type, torch.cuda.current_device())
     if stream is None:
         handle = torch.cuda.current_stream(dev).cuda_stream
-    elif isinstance(stream, torch.cuda.Stream):
-        handle = stream.cuda_stream
     else:
-        handle = int(stream)
+        handle = int(getattr(stream, "cuda_stream", stream))
     key = (dev.index, handle)
     ws = _workspaces.get(key)
     if ws is None:
-        ws = empty_workspace(dev)
+        ws = _clear_workspace(dev, stream)
         _workspaces[key] = ws
     return ws
 
@@ -527,16 +541,6 @@ def _on(x: torch.Tensor, what: str) -> torch.device:
     if not isinstance(x, torch.Tensor) or not x.is_cuda or not x.is_contiguous():
         raise ValueError(f"{what} must be a contiguous CUDA tensor")
     return x.device
-
-
-def _under(stream, device):
-    """The context of a call that was given a stream of its own: torch's, an
-    object with its handle in cuda_stream, or the handle."""
-    if not isinstance(stream, torch.cuda.Stream):
-        handle = int(getattr(stream, "cuda_stream", stream))
-        # ExternalStream takes 0, the default stream's handle, for none given and makes a new stream
-        stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
-    return torch.cuda.stream(stream)
 
 
 def _current(device) -> int:

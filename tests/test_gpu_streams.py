@@ -65,3 +65,18 @@ def test_the_stream_that_was_given_is_the_one_launched_on(monkeypatch, name):
     torch.cuda.synchronize()
     assert recorder.handles == [0, 0, 0] + [side.cuda_stream] * 3 + [other.cuda_stream]
     assert all(torch.equal(g, want) for g in got)
+
+
+def test_a_grouped_call_clears_its_workspace_on_its_stream(monkeypatch):
+    x = torch.randn((64, 128), device=DEV)
+    want, _ = nv.quantize_grouped(x, [16, 48], columnwise=False)
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    cleared_on, real = [], nv.empty_workspace
+    monkeypatch.setattr(nv, "empty_workspace", lambda device: cleared_on.append(torch.cuda.current_stream().cuda_stream) or real(device))
+    with torch.cuda.stream(other):
+        got = [nv.quantize_grouped(x, [16, 48], columnwise=False, stream=s)[0] for s in (0, side, side.cuda_stream, None)]
+    torch.cuda.synchronize()
+    assert cleared_on == [0, side.cuda_stream, side.cuda_stream, other.cuda_stream]
+    for g in got:
+        assert torch.equal(g.data, want.data) and torch.equal(g.scales, want.scales) and torch.equal(g.amax, want.amax)

@@ -37,3 +37,13 @@ def test_a_stream_by_its_handle(entered, stream, handle):
     with nv._under(stream, DEV):
         pass
     assert entered == [handle]
+
+
+@pytest.mark.parametrize("stream,handle", [(0, 0), (0x7000, 0x7000), (types.SimpleNamespace(cuda_stream=0x7100), 0x7100)])
+def test_a_workspace_is_cleared_on_the_stream_that_uses_it(entered, monkeypatch, stream, handle):
+    monkeypatch.setattr(nv, "_workspaces", {})
+    cleared = []
+    monkeypatch.setattr(nv, "empty_workspace", lambda device: cleared.append((device, list(entered))) or object())
+    ws = nv.stream_workspace(DEV, stream)
+    assert cleared == [(DEV, [handle])]
+    assert nv.stream_workspace(DEV, handle) is ws and len(cleared) == 1
