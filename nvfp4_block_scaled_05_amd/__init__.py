@@ -17,6 +17,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import dataclasses
+import functools
 import os
 from typing import Optional
 
@@ -205,6 +206,36 @@ def _under(stream, device):
     return torch.cuda.stream(stream)
 
 
+def _current_device() -> int:
+    # torch.cuda.current_device() without its check for a first use, which a tensor on a GPU has behind it
+    return torch._C._cuda_getDevice()
+
+
+def _elsewhere(stream, device):
+    """The context that a call on tensors of `device` enters before it goes on:
+    that of its stream, or of the device where that is not the current one (the
+    library launches on the current one). None if neither is needed."""
+    if stream is not None:
+        if getattr(stream, "device", device) != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        return _under(stream, device)
+    return None if _current_device() == device.index else torch.cuda.device(device)
+
+
+def _on_its_device(call):
+    """`call` with the device of its first argument as the current one."""
+    @functools.wraps(call)
+    def guarded(*args, **kwargs):
+        x = args[0] if args else next(iter(kwargs.values()), None)
+        t = x if isinstance(x, torch.Tensor) else getattr(x, "data", None)
+        index = t.get_device() if isinstance(t, torch.Tensor) else -1  # -1: not on a GPU, which the call refuses
+        if index < 0 or index == _current_device():
+            return call(*args, **kwargs)
+        with torch.cuda.device(index):
+            return call(*args, **kwargs)
+    return guarded
+
+
 def _shape2d(x: torch.Tensor):
     if x.dim() != 2 or not x.is_contiguous() or not x.is_cuda:
         raise ValueError("x must be a contiguous 2-D CUDA tensor")
@@ -269,6 +300,7 @@ def nvfp4_workspace_bytes() -> int:
     return int(load().nvfp4_workspace_bytes())
 
 
+@_on_its_device
 def nvfp4_compute_amax(x: torch.Tensor, row_amax: Optional[torch.Tensor], col_amax: Optional[torch.Tensor],
                        cfg: Optional[nvfp4_config_t] = None, stream=None) -> None:
     rows, cols = _shape2d(x)
@@ -280,6 +312,7 @@ def nvfp4_compute_amax(x: torch.Tensor, row_amax: Optional[torch.Tensor], col_am
                                      None if cfg is None else ctypes.byref(cfg), _stream(stream)))
 
 
+@_on_its_device
 def nvfp4_quantize(x: torch.Tensor, row: Optional[Orientation], col: Optional[Orientation],
                    cfg: Optional[nvfp4_config_t] = None, stream=None) -> None:
     rows, cols = _shape2d(x)
@@ -292,6 +325,7 @@ def nvfp4_quantize(x: torch.Tensor, row: Optional[Orientation], col: Optional[Or
                                  _stream(stream)))
 
 
+@_on_its_device
 def nvfp4_quantize_noalloc(x: torch.Tensor, row: Optional[Orientation], col: Optional[Orientation],
                            cfg: Optional[nvfp4_config_t] = None, stream=None) -> None:
     """nvfp4_quantize with the library's own per-device scratch in place of a
@@ -306,6 +340,7 @@ def nvfp4_quantize_noalloc(x: torch.Tensor, row: Optional[Orientation], col: Opt
                                          None if cfg is None else ctypes.byref(cfg), _stream(stream)))
 
 
+@_on_its_device
 def nvfp4_dequantize(q: Orientation, rows: int, cols: int, scale_layout: int, row_scaled: bool, y: torch.Tensor,
                      stream=None, scale_fmt: int = 0) -> None:
     _need_orientation(q, rows, cols, rows if row_scaled else 1, "quantized tensor")
@@ -315,6 +350,7 @@ def nvfp4_dequantize(q: Orientation, rows: int, cols: int, scale_layout: int, ro
                                    _stream(stream)))
 
 
+@_on_its_device
 def nvfp4_quantize_grouped(x: torch.Tensor, group_rows, row: Optional[Orientation], col: Optional[Orientation],
                            cfg: Optional[nvfp4_config_t] = None, stream=None) -> None:
     """x [sum(group_rows)][C]; row/col hold the concatenated per-group outputs
@@ -330,6 +366,7 @@ def nvfp4_quantize_grouped(x: torch.Tensor, group_rows, row: Optional[Orientatio
                                          None if cfg is None else ctypes.byref(cfg), _stream(stream)))
 
 
+@_on_its_device
 def quantize_grouped(x: torch.Tensor, group_rows, *, rowwise=True, columnwise=True,
                      cfg: Optional[nvfp4_config_t] = None, stream=None, use_workspace: bool = True):
     """Allocate the concatenated per-group outputs and run nvfp4_quantize_grouped.
@@ -362,6 +399,7 @@ def nvfp4_swizzled_scales_bytes(rows: int, scale_cols: int) -> int:
     return int(load().nvfp4_swizzled_scales_bytes(rows, scale_cols))
 
 
+@_on_its_device
 def nvfp4_swizzle_scales(compact: torch.Tensor, rows: int, scale_cols: int, swizzled: torch.Tensor,
                          stream=None) -> None:
     """compact: uint8 with rows * scale_cols bytes; swizzled: uint8 with
@@ -371,6 +409,7 @@ def nvfp4_swizzle_scales(compact: torch.Tensor, rows: int, scale_cols: int, swiz
     _check(load().nvfp4_swizzle_scales(_ptr(compact), rows, scale_cols, _ptr(swizzled), _stream(stream)))
 
 
+@_on_its_device
 def nvfp4_debug_rht_colwise(x: torch.Tensor, sign_mask: int, t: torch.Tensor, stream=None) -> None:
     rows, cols = _shape2d(x)
     _need(t, rows * cols, torch.float32, "t")
@@ -378,6 +417,7 @@ def nvfp4_debug_rht_colwise(x: torch.Tensor, sign_mask: int, t: torch.Tensor, st
                                           _stream(stream)))
 
 
+@_on_its_device
 def nvfp4_debug_e2m1_pack(v: torch.Tensor, r: Optional[torch.Tensor], out: torch.Tensor, flags: int,
                           stream=None) -> None:
     """v: float32 [2n]; r: int32/uint32 [n] or None; out: uint8 [n]."""
@@ -451,6 +491,7 @@ def nvfp4_debug_set_rht_unit(unit: int) -> None:
     _check(load().nvfp4_debug_set_rht_unit(int(unit) & 0xFFFFFFFF))
 
 
+@_on_its_device
 def quantize(x: torch.Tensor, *, rowwise=True, columnwise=True, cfg: Optional[nvfp4_config_t] = None,
              stream=None, use_workspace: bool = True):
     """Allocate outputs for x [R][C] and run nvfp4_quantize. Returns (row, col).
@@ -571,8 +612,8 @@ def expert_sort(ids: torch.Tensor, experts: int, *, align: int = FP8_BLOCK, rows
     tokens, topk = ids.shape
     if rows is None:
         rows = int(lib.nvfp4_expert_rows(tokens, topk, experts, align))
-    if stream is not None:
-        with _under(stream, dev):
+    if (context := _elsewhere(stream, dev)) is not None:
+        with context:
             return expert_sort(ids, experts, align=align, rows=rows)
     # one allocation for all five arrays (each costs more than cutting them apart)
     sizes = (tokens * topk, max(rows, 0), max(experts, 0) + 1, max(experts, 0),
@@ -591,8 +632,8 @@ def expert_gather(x: torch.Tensor, plan: ExpertPlan, *, stream=None) -> torch.Te
     if x.dim() != 2 or x.shape[0] != plan.tokens:
         raise ValueError(f"x must be [{plan.tokens}][cols], got {tuple(x.shape)}")
     code = _dtype_code(x)
-    if stream is not None:
-        with _under(stream, dev):
+    if (context := _elsewhere(stream, dev)) is not None:
+        with context:
             return expert_gather(x, plan)
     y = torch.empty((plan.rows, x.shape[1]), dtype=x.dtype, device=dev)
     _check(load().nvfp4_expert_gather(x.data_ptr(), code, plan.tokens, plan.topk, x.shape[1], plan.slot_rows.data_ptr(),
@@ -611,8 +652,8 @@ def expert_combine(y: torch.Tensor, plan: ExpertPlan, weights: Optional[torch.Te
     if weights is not None:
         _want(weights, torch.float32, (plan.tokens, plan.topk), dev, "weights")
     code = _dtype_code(y)
-    if stream is not None:
-        with _under(stream, dev):
+    if (context := _elsewhere(stream, dev)) is not None:
+        with context:
             return expert_combine(y, plan, weights)
     out = torch.empty((plan.tokens, y.shape[1]), dtype=y.dtype, device=dev)
     _check(load().nvfp4_expert_combine(y.data_ptr(), code, plan.tokens, plan.topk, y.shape[1], plan.slot_rows.data_ptr(), plan.rows,
@@ -636,8 +677,8 @@ def expert_combine_grad(dout: torch.Tensor, y: torch.Tensor, plan: ExpertPlan, w
     _want(y, dout.dtype, (plan.rows, cols), dev, "y")
     _want(weights, torch.float32, (plan.tokens, plan.topk), dev, "weights")
     code = _dtype_code(dout)
-    if stream is not None:
-        with _under(stream, dev):
+    if (context := _elsewhere(stream, dev)) is not None:
+        with context:
             return expert_combine_grad(dout, y, plan, weights)
     dy = torch.empty((plan.rows, cols), dtype=dout.dtype, device=dev)
     dw = torch.empty((plan.tokens, plan.topk), dtype=torch.float32, device=dev)
@@ -672,8 +713,8 @@ def fp8_quantize(x: torch.Tensor, *, rowwise=True, columnwise=False, block_2d=Fa
         if rows != plan.tokens:
             raise ValueError(f"x must be [{plan.tokens}][cols], got {tuple(x.shape)}")
         slots, tokens, topk, rows = plan.row_slots, plan.tokens, plan.topk, plan.rows
-    if stream is not None:
-        with _under(stream, dev):
+    if (context := _elsewhere(stream, dev)) is not None:
+        with context:
             return fp8_quantize(x, rowwise=rowwise, columnwise=columnwise, block_2d=block_2d, plan=plan)
 
     def empty(n, k):
@@ -709,8 +750,8 @@ def fp8_matmul(a: Fp8Tensor, b: Fp8Tensor, *, out_dtype=torch.bfloat16, stream=N
     code = _out_code(out_dtype)
     _want_fp8(a, (), a.n, a.k, False, dev, "operand a")
     _want_fp8(b, (), b.n, a.k, bool(b.block_2d), dev, "operand b")
-    if stream is not None:
-        with _under(stream, dev):
+    if (context := _elsewhere(stream, dev)) is not None:
+        with context:
             return fp8_matmul(a, b, out_dtype=out_dtype)
     d = torch.empty((a.n, b.n), dtype=out_dtype, device=dev)
     _check(load().nvfp4_fp8_matmul(a.as_c(), b.as_c(), a.n, b.n, a.k, int(b.block_2d), d.data_ptr(), code, _current(dev)))
@@ -726,8 +767,8 @@ def fp8_matmul_grouped(a: Fp8Tensor, b: Fp8Tensor, plan: ExpertPlan, *, out_dtyp
     _want_plan(plan, dev)
     _want_fp8(a, (), plan.rows, a.k, False, dev, "operand a")
     _want_fp8(b, (plan.experts,), b.n, a.k, True, dev, "operand b")
-    if stream is not None:
-        with _under(stream, dev):
+    if (context := _elsewhere(stream, dev)) is not None:
+        with context:
             return fp8_matmul_grouped(a, b, plan, out_dtype=out_dtype)
     d = torch.empty((plan.rows, b.n), dtype=out_dtype, device=dev)
     _check(load().nvfp4_fp8_matmul_grouped(a.as_c(), b.as_c(), plan.offsets.data_ptr(), plan.experts, plan.rows, b.n, a.k,
@@ -746,8 +787,8 @@ def fp8_matmul_grouped_k(a: Fp8Tensor, b: Fp8Tensor, plan: ExpertPlan, *, out_dt
         raise ValueError(f"the plan must be aligned to {FP8_BLOCK} rows, got {plan.align}")
     _want_fp8(a, (), a.n, plan.rows, False, dev, "operand a")
     _want_fp8(b, (), b.n, plan.rows, False, dev, "operand b")
-    if stream is not None:
-        with _under(stream, dev):
+    if (context := _elsewhere(stream, dev)) is not None:
+        with context:
             return fp8_matmul_grouped_k(a, b, plan, out_dtype=out_dtype)
     d = torch.empty((plan.experts, a.n, b.n), dtype=out_dtype, device=dev)
     _check(load().nvfp4_fp8_matmul_grouped_k(a.as_c(), b.as_c(), plan.offsets.data_ptr(), plan.experts, a.n, b.n, plan.rows,

@@ -80,3 +80,19 @@ def test_a_grouped_call_clears_its_workspace_on_its_stream(monkeypatch):
     assert cleared_on == [0, side.cuda_stream, side.cuda_stream, other.cuda_stream]
     for g in got:
         assert torch.equal(g.data, want.data) and torch.equal(g.scales, want.scales) and torch.equal(g.amax, want.amax)
+
+
+@pytest.mark.parametrize("name", ["sort", "gather", "combine", "gather_grad", "combine_grad", "quantize", "matmul", "grouped", "grouped_k"])
+def test_the_tensors_device_is_made_the_current_one(monkeypatch, name):
+    call = calls()[name]
+    want = call(None)
+    entered = []
+
+    class Noted(torch.cuda.device):
+        def __enter__(self):
+            entered.append(self.idx)
+            return super().__enter__()
+
+    monkeypatch.setattr(nv, "_current_device", lambda: 0 if entered else 1)
+    monkeypatch.setattr(torch.cuda, "device", Noted)
+    assert torch.equal(call(None), want) and entered == [want.device.index]
