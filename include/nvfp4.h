@@ -489,7 +489,9 @@ nvfp4_status_t nvfp4_fp8_quantize(const void *x, nvfp4_dtype_t dtype, int64_t ba
  * row-wise, dx = dy w takes dy row-wise and w column-wise, dw = dy^T x takes
  * both column-wise. Scales may be any FP32 numbers, also where the product of
  * two leaves FP32's range; but tiles that meet such a pair (b in 1x128 blocks: a
- * scale of a outside 2^-108 .. 2^103) take some ten times as long.
+ * scale of a outside 2^-108 .. 2^103) take some ten times as long. One launch: an
+ * output whose tiles take 2^32 threads (2^24 tiles of 128x128, or as many parts of
+ * one) is refused as a shape.
  */
 nvfp4_status_t nvfp4_fp8_matmul(const nvfp4_fp8_t *a, const nvfp4_fp8_t *b, int64_t m, int64_t n, int64_t k,
                                 uint32_t b_block_2d, void *d, nvfp4_dtype_t d_dtype, void *stream);

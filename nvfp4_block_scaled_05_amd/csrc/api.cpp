@@ -653,7 +653,10 @@ nvfp4_status_t matmul(const nvfp4_fp8_t *a, const nvfp4_fp8_t *b, int64_t rows, 
   p.mode = mode;
   p.offsets = offsets;
   p.groups = static_cast<uint32_t>(groups);
-  return hip_status(nvfp4::launch_fp8_matmul(p, static_cast<hipStream_t>(stream)), "FP8 product launch");
+  const hipError_t e = nvfp4::launch_fp8_matmul(p, static_cast<hipStream_t>(stream));
+  if (e == hipErrorInvalidConfiguration)
+    return fail(NVFP4_ERR_SHAPE, "an output of %lld x %lld is too large for one launch", (long long)rows, (long long)n);
+  return hip_status(e, "FP8 product launch");
 }
 
 }  // namespace

@@ -289,7 +289,7 @@ __global__ __launch_bounds__(kRowThreads) void k_expert_gather(const typename El
                                                                typename Elem<DT>::type *__restrict__ y) {
   constexpr uint32_t per = Elem<DT>::per;
   const uint32_t lane = threadIdx.x % kWave;
-  const uint64_t unit = static_cast<uint64_t>(blockIdx.x) * kRowWaves + wave_index(), units = static_cast<uint64_t>(tokens) * strips;
+  const uint64_t unit = static_cast<uint64_t>(block_of_long_grid()) * kRowWaves + wave_index(), units = static_cast<uint64_t>(tokens) * strips;
   if (unit >= units) {
     clear_padding<DT>(y, row_slots, (unit - units) * kPadRows, tokens * topk, cols, rows, lane);
     return;
@@ -329,7 +329,7 @@ __global__ __launch_bounds__(kRowThreads) void k_expert_combine(const typename E
                                                                 uint32_t strips, typename Elem<DT>::type *__restrict__ out) {
   constexpr uint32_t per = Elem<DT>::per;
   const uint32_t lane = threadIdx.x % kWave;
-  const uint64_t unit = static_cast<uint64_t>(blockIdx.x) * kRowWaves + wave_index();
+  const uint64_t unit = static_cast<uint64_t>(block_of_long_grid()) * kRowWaves + wave_index();
   const uint32_t token = static_cast<uint32_t>(unit / strips), strip = static_cast<uint32_t>(unit % strips);
   if (token >= tokens) return;
   const int32_t *at = slot_rows + static_cast<uint64_t>(token) * topk;
@@ -382,7 +382,7 @@ __global__ __launch_bounds__(kRowThreads) void k_expert_combine_grad(
     float *__restrict__ dw) {
   constexpr uint32_t per = Elem<DT>::per;
   const uint32_t lane = threadIdx.x % kWave;
-  const uint64_t unit = static_cast<uint64_t>(blockIdx.x) * kRowWaves + wave_index();
+  const uint64_t unit = static_cast<uint64_t>(block_of_long_grid()) * kRowWaves + wave_index();
   if (unit >= slots) {
     clear_padding<DT>(dy, row_slots, (unit - slots) * kPadRows, slots, cols, rows, lane);
     return;
@@ -466,7 +466,7 @@ static hipError_t gather_t(const ExpertRows &p, hipStream_t s) {
   typedef typename Elem<DT>::type T;
   const uint32_t strips = static_cast<uint32_t>(blocks_of(p.cols, kGatherPieces * kWave * Elem<DT>::per));
   const uint64_t units = static_cast<uint64_t>(p.tokens) * strips + blocks_of(p.rows, kPadRows);
-  hipLaunchKernelGGL((k_expert_gather<DT>), dim3(static_cast<uint32_t>(blocks_of(units, kRowWaves))), dim3(kRowThreads), 0, s,
+  hipLaunchKernelGGL((k_expert_gather<DT>), long_grid(blocks_of(units, kRowWaves)), dim3(kRowThreads), 0, s,
                      static_cast<const T *>(p.x), p.slot_rows, p.row_slots, p.tokens, p.topk, p.cols, p.rows, strips,
                      static_cast<T *>(p.out));
   return hipGetLastError();
@@ -477,7 +477,7 @@ static hipError_t combine_t(const ExpertRows &p, hipStream_t s) {
   typedef typename Elem<DT>::type T;
   const uint32_t strips = static_cast<uint32_t>(blocks_of(p.cols, kWave * Elem<DT>::per));
   const uint64_t blocks = blocks_of(static_cast<uint64_t>(p.tokens) * strips, kRowWaves);
-  hipLaunchKernelGGL((k_expert_combine<DT>), dim3(static_cast<uint32_t>(blocks)), dim3(kRowThreads), 0, s,
+  hipLaunchKernelGGL((k_expert_combine<DT>), long_grid(blocks), dim3(kRowThreads), 0, s,
                      static_cast<const T *>(p.x), p.slot_rows, p.weights, p.tokens, p.topk, p.cols, p.rows, strips,
                      static_cast<T *>(p.out));
   return hipGetLastError();
@@ -487,7 +487,7 @@ template <int DT>
 static hipError_t combine_grad_t(const ExpertRows &p, hipStream_t s) {
   typedef typename Elem<DT>::type T;
   const uint64_t units = static_cast<uint64_t>(p.tokens) * p.topk + blocks_of(p.rows, kPadRows);
-  hipLaunchKernelGGL((k_expert_combine_grad<DT>), dim3(static_cast<uint32_t>(blocks_of(units, kRowWaves))), dim3(kRowThreads), 0,
+  hipLaunchKernelGGL((k_expert_combine_grad<DT>), long_grid(blocks_of(units, kRowWaves)), dim3(kRowThreads), 0,
                      s, static_cast<const T *>(p.x), static_cast<const T *>(p.y), p.slot_rows, p.row_slots, p.weights,
                      p.tokens * p.topk, p.topk, p.cols, p.rows, static_cast<T *>(p.out), p.dweights);
   return hipGetLastError();

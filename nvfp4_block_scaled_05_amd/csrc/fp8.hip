@@ -59,6 +59,7 @@ struct Args {
   const void *x;
   uint32_t rows, cols;             // of one matrix
   uint32_t row_tiles, col_tiles;
+  uint32_t tiles;                  // of all matrices
   const int32_t *row_slots;
   uint32_t slots, topk;
   uint8_t *row_data, *col_data;
@@ -189,7 +190,9 @@ __global__ __launch_bounds__(kThreads) void k_fp8_quantize(Args a) {
   __shared__ float row_mult[kTile], col_mult[kTile];
   __shared__ u32x2 turned[kTile][16];  // the transposed tile's codes, 8 bytes apiece, see below
   const uint32_t t = threadIdx.x, cg = t % 16, rg = t / 16, lane = t % 64, wave = t / 64;
-  const uint32_t per_batch = a.row_tiles * a.col_tiles, batch = blockIdx.x / per_batch, id = blockIdx.x - batch * per_batch;
+  const uint32_t block = block_of_long_grid();
+  if (block >= a.tiles) return;
+  const uint32_t per_batch = a.row_tiles * a.col_tiles, batch = block / per_batch, id = block - batch * per_batch;
   uint32_t ct = id % a.col_tiles, rt = id / a.col_tiles;
   if (a.row_slots != nullptr) {
     // a token's row is read topk times: an XCD (workgroups go to the eight in
@@ -297,11 +300,10 @@ __global__ __launch_bounds__(kThreads) void k_fp8_quantize(Args a) {
 namespace {
 
 template <int DT, bool BLOCK_2D>
-hipError_t launch(const Args &a, uint32_t batch, hipStream_t s) {
-  const uint64_t tiles = static_cast<uint64_t>(batch) * a.row_tiles * a.col_tiles;
-  if (tiles == 0) return hipSuccess;
-  const uint64_t out = tiles * kTile * kTile * ((a.row_data != nullptr) + (a.col_data != nullptr));
-  const dim3 grid(static_cast<uint32_t>(tiles));
+hipError_t launch(const Args &a, hipStream_t s) {
+  if (a.tiles == 0) return hipSuccess;
+  const uint64_t out = static_cast<uint64_t>(a.tiles) * kTile * kTile * ((a.row_data != nullptr) + (a.col_data != nullptr));
+  const dim3 grid = long_grid(a.tiles);
   if (out > kL2Bytes && a.row_data != nullptr) hipLaunchKernelGGL((k_fp8_quantize<DT, BLOCK_2D, true>), grid, dim3(kThreads), kSpareLds, s, a);
   else hipLaunchKernelGGL((k_fp8_quantize<DT, BLOCK_2D, false>), grid, dim3(kThreads), kSpareLds, s, a);
   return hipGetLastError();
@@ -310,10 +312,11 @@ hipError_t launch(const Args &a, uint32_t batch, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_fp8_quantize(const Fp8Quantize &p, int dtype, bool block_2d, hipStream_t s) {
-  const Args a{p.x, p.rows, p.cols, (p.rows + kTile - 1) / kTile, (p.cols + kTile - 1) / kTile, p.row_slots, p.slots, p.topk,
+  const uint32_t row_tiles = (p.rows + kTile - 1) / kTile, col_tiles = (p.cols + kTile - 1) / kTile;
+  const Args a{p.x, p.rows, p.cols, row_tiles, col_tiles, p.batch * row_tiles * col_tiles, p.row_slots, p.slots, p.topk,
                p.row_data, p.col_data, p.row_scales, p.col_scales};
-  if (dtype == kBF16) return block_2d ? launch<kBF16, true>(a, p.batch, s) : launch<kBF16, false>(a, p.batch, s);
-  return block_2d ? launch<kFP32, true>(a, p.batch, s) : launch<kFP32, false>(a, p.batch, s);
+  if (dtype == kBF16) return block_2d ? launch<kBF16, true>(a, s) : launch<kBF16, false>(a, s);
+  return block_2d ? launch<kFP32, true>(a, s) : launch<kFP32, false>(a, s);
 }
 
 }  // namespace nvfp4

@@ -721,7 +721,9 @@ hipError_t launch_rows(const Fp8Matmul &p, hipStream_t s) {
   Args a{p.a, p.b, p.sa, p.sb, p.d, p.m, p.n, p.kblocks, p.sa_stride, p.sb_stride, p.mode, p.offsets, p.groups, 0, 0};
   a.tiles_n = (p.n + kRowsN - 1) / kRowsN;
   a.tiles_m = p.mode == kGroupedRows ? p.m / kRowsM + p.groups + 1 : (p.m + kRowsM - 1) / kRowsM;
-  const dim3 grid(a.tiles_m * a.tiles_n), threads(KS * kWave);
+  const uint64_t blocks = static_cast<uint64_t>(a.tiles_m) * a.tiles_n;
+  if (blocks * KS * kWave >= kMaxThreads1D) return hipErrorInvalidConfiguration;
+  const dim3 grid(static_cast<uint32_t>(blocks)), threads(KS * kWave);
   if (p.b_block_2d) {
     if (p.out_fp32) hipLaunchKernelGGL((k_fp8_rows<KS, false, true>), grid, threads, 0, s, a);
     else hipLaunchKernelGGL((k_fp8_rows<KS, false, false>), grid, threads, 0, s, a);
@@ -742,7 +744,7 @@ hipError_t launch_tile(const Fp8Matmul &p, hipStream_t s) {
   if (p.mode == kGroupedRows) rows = p.m / BM + p.groups + 1;
   if (p.mode == kGroupedK) rows = static_cast<uint64_t>(a.tiles_m) * p.groups;
   const uint64_t blocks = rows * a.tiles_n;
-  if (blocks >= (uint64_t{1} << 31)) return hipErrorInvalidConfiguration;
+  if (blocks * WM * WN * KS * kWave >= kMaxThreads1D) return hipErrorInvalidConfiguration;
   const dim3 grid(static_cast<uint32_t>(blocks)), threads(WM * WN * KS * kWave);
   if (p.b_block_2d) {
     if (p.out_fp32) hipLaunchKernelGGL((k_fp8_tile<BM, BN, WM, WN, KS, PHASED, false, true>), grid, threads, 0, s, a);

@@ -198,8 +198,18 @@ hipError_t launch_dequant(const uint8_t *data, const uint8_t *scales, const floa
 uint64_t swizzled_scales_bytes(uint64_t rows, uint64_t scale_cols);
 hipError_t launch_swizzle(const uint8_t *compact, uint32_t rows, uint32_t scale_cols, uint8_t *out, hipStream_t s);
 
+// A launch has fewer than 2^32 threads along x (the runtime takes more without an
+// error and runs what is left of them modulo 2^32), so the workgroups past
+// kGridX go on along y. The last line may have more than there is work for.
+constexpr uint32_t kGridX = 1u << 22;  // workgroups; times up to 1023 threads
+constexpr uint64_t kMaxThreads1D = uint64_t{1} << 32;
+inline dim3 long_grid(uint64_t blocks) {
+  return blocks <= kGridX ? dim3(static_cast<uint32_t>(blocks)) : dim3(kGridX, static_cast<uint32_t>((blocks + kGridX - 1) / kGridX));
+}
+__device__ __forceinline__ uint32_t block_of_long_grid() { return blockIdx.y * kGridX + blockIdx.x; }
+
 // Tokens by expert. Validated by the caller: tokens * topk < 2^31, rows <
-// 2^31, cols < 2^31, experts in 1 .. kMaxGroups, grids below 2^31 blocks.
+// 2^31, cols < 2^31, experts in 1 .. kMaxGroups, below 2^31 workgroups.
 struct ExpertSort {
   const void *ids;
   uint32_t wide;  // 64-bit ids
