@@ -287,10 +287,12 @@ template <int DT, bool SR, bool COMPUTE>
 __global__ __launch_bounds__(kThreads) void k_rowscaled(RowScaledArgs p) {
   __shared__ uint32_t lds_w[kWaves];
   if (p.noop != nullptr && *p.noop == 1.0f) return;
+  const uint32_t row = block_of_long_grid();
+  if (row >= p.rows) return;
   const uint32_t key = SR ? sr_key(p.sr_seed, 0) : 0u;
   Block<DT> a[kRegBlocks];
-  load_row<DT>(p, blockIdx.x, a);
-  process_row<DT, SR, COMPUTE>(p, blockIdx.x, a, lds_w, key, 0);
+  load_row<DT>(p, row, a);
+  process_row<DT, SR, COMPUTE>(p, row, a, lds_w, key, 0);
 }
 
 // Grouped form (row slices, each a row-scaled tensor of its own): the same
@@ -301,11 +303,13 @@ template <int DT, bool COMPUTE>
 __global__ __launch_bounds__(kThreads) void k_rowscaled_grouped(RowScaledArgs p, GroupTable t) {
   __shared__ uint32_t lds_w[kWaves];
   if (p.noop != nullptr && *p.noop == 1.0f) return;
+  const uint32_t row = block_of_long_grid();
+  if (row >= p.rows) return;
   const uint32_t key = sr_key(p.sr_seed, 0);
-  const uint32_t g = group_of(t, blockIdx.x);
+  const uint32_t g = group_of(t, row);
   Block<DT> a[kRegBlocks];
-  load_row<DT>(p, blockIdx.x, a);
-  process_row<DT, true, COMPUTE>(p, blockIdx.x, a, lds_w, key,
+  load_row<DT>(p, row, a);
+  process_row<DT, true, COMPUTE>(p, row, a, lds_w, key,
                                  static_cast<uint64_t>(t.unit_start[g]) * (p.cols >> 1));
 }
 
@@ -482,7 +486,7 @@ __global__ __launch_bounds__(kThreads) void k_dual_amax(RowScaledArgs p, float *
 
 template <int DT, bool SR, bool COMPUTE>
 hipError_t launch_one(const RowScaledArgs &a, hipStream_t s) {
-  hipLaunchKernelGGL((k_rowscaled<DT, SR, COMPUTE>), dim3(a.rows), dim3(kThreads), 0, s, a);
+  hipLaunchKernelGGL((k_rowscaled<DT, SR, COMPUTE>), long_grid(a.rows), dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 
@@ -524,7 +528,7 @@ hipError_t launch_rowscaled_grouped(const RowScaledArgs &a, const uint32_t *row_
   GroupTable t{};
   t.ngroups = ngroups;
   for (uint32_t g = 0; g <= ngroups; ++g) t.unit_start[g] = t.row_start[g] = row_start[g];
-  const dim3 grid(a.rows), block(kThreads);
+  const dim3 grid = long_grid(a.rows), block(kThreads);
   if (dtype == kBF16) {
     if (compute_amax)
       hipLaunchKernelGGL((k_rowscaled_grouped<kBF16, true>), grid, block, 0, s, a, t);

@@ -41,3 +41,27 @@ def test_quantize_of_more_matrices_than_one_grid_line_has_tiles(block_2d):
         code = torch.where(x[:, 0, 0] == 0, 0, 0x7E).to(torch.uint8) | (x[:, 0, 0].view(torch.int16) < 0).to(torch.uint8) * 128
         assert torch.equal(codes[:, 0], code)
         assert not bool(codes[:, 1:].any())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_row_scaled_tensor_of_more_rows_than_one_grid_line_has(dtype):
+    rows, cols, tail = (1 << 24) + 256, 16, 512
+    x = torch.randn((rows, cols), device=DEV, generator=torch.Generator(DEV).manual_seed(3)).to(dtype)
+    amax = x.float().abs().amax(1)
+    row, _ = nv.quantize(x, columnwise=False, cfg=nv.make_config(row_scaled=True))
+    assert torch.equal(row.amax, amax)
+    last, _ = nv.quantize(x[-tail:].contiguous(), columnwise=False, cfg=nv.make_config(row_scaled=True))
+    assert torch.equal(row.data[-tail:], last.data) and torch.equal(row.scales[-tail:], last.scales)
+    only = torch.zeros(rows, device=DEV)
+    nv.nvfp4_compute_amax(x, only, None, nv.make_config(row_scaled=True))
+    assert torch.equal(only, amax)
+
+
+def test_row_scaled_groups_of_more_rows_than_one_grid_line_has():
+    rows, cols, tail = (1 << 24) + 256, 16, 512
+    x = torch.randn((rows, cols), device=DEV, generator=torch.Generator(DEV).manual_seed(4)).to(torch.bfloat16)
+    cfg = dict(row_scaled=True, stochastic=True, sr_seed=3)
+    row, _ = nv.quantize_grouped(x, [rows - tail, tail], columnwise=False, cfg=nv.make_config(**cfg))
+    assert torch.equal(row.amax, x.float().abs().amax(1))
+    last, _ = nv.quantize_grouped(x[-tail:].contiguous(), [tail], columnwise=False, cfg=nv.make_config(**cfg))
+    assert torch.equal(row.data[-tail * cols // 2:], last.data) and torch.equal(row.scales[-tail * cols // 16:], last.scales)
