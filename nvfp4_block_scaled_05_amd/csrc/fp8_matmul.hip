@@ -758,26 +758,32 @@ hipError_t launch_tile(const Fp8Matmul &p, hipStream_t s) {
 
 }  // namespace
 
-// Which kernel. Times in us.
-//   Few rows, against the 64x64 tiles below: m up to 32, or 24 a group on average, by the buffer's rows:
-//     16 x 8192 x 5120        9.8 / 16.2         32 x 4096 x 4096  10.1 / 12.9
-//     64 groups, 1472 rows x 4096 x 2048  107 / 120
-//     but 64 x 8192 x 5120    17.8 / 16.6;       32 groups, 992 rows x 2048 x 2048  35 / 34 in 128x128
+// Which kernel. Times in us, of one session.
+//   Few rows, against the 64x64 tiles below: m up to 32:
+//     16 x 8192 x 5120        9.9 / 16.7         32 x 4096 x 4096  10.3 / 13.6
+//     32 x 8192 x 5120       12.5 / 17.0;  but   64 x 8192 x 5120  17.7 / 17.2
+//   or up to 32 a group on average, by the buffer's rows, against 128x128 tiles:
+//     64 groups, 1472 rows x 4096 x 2048  106 / 130     52 groups, 1280 rows  90 / 112
+//     32 groups,  992 rows x 4096 x 2048   56 / 63      the same x 2048 x 2048  31 / 33
+//     64 groups, 1792 rows x 4096 x 2048  147 / 154;  at 2048 rows both 157
 //   Up to 160 tiles of 128x128 they leave CUs idle, and a wave that has its
 //   SIMD to itself takes 0.5 us a step, most of it waiting for its own last
 //   instruction. So up to 256 tiles of 64x64 (one a CU) those, with 16 waves in
 //   four shares of the blocks along k, against four waves and against 128x128:
-//     256 x 4096 x 4096       15.1 / 19.8 / 39   256 x 1024 x 8192  23 / 34
+//     256 x 4096 x 4096       15.3 / 20.0 / 40   256 x 1024 x 8192  24 / 36 / 75
 //   and above that 64x128 tiles with 8 waves in two shares, against 64x64 with four waves:
-//     777 x 1361 x 1999       15.1 / 16.4        512 x 4096 x 4096  24 / 29
-//     but 1024 x 4096 x 2048 (256 tiles of 128x128)  26.6, and 128x128 24.7
+//     777 x 1361 x 1999       15.1 / 16.1        512 x 4096 x 4096  24 / 27
+//     but 1280 x 2048 x 4096 (160 tiles of 128x128)  43 / 35, and 128x128 40;
+//     1024 x 4096 x 2048 (256 tiles of 128x128)  24.6, and 128x128, which it takes, 23.4
 //   256x256 tiles, phased, where their rounds over 256 CUs, 3.1 us a step along
 //   k, take less than those of 128x128 tiles over 512 places, 1.8 us a step:
-//     8192 x 8192 x 5120      500 / 580          4096 x 4096 x 4096  117 / 132
-//     8 groups, 66552 rows x 4096 x 2048  939 / 1007;   32 weight gradients of 4096 x 2048  688 / 720
-//     but 3000 x 8192 x 5120  253 / 229
+//     8192 x 8192 x 5120      516 / 607          4096 x 4096 x 4096  107 / 126
+//     8 groups, 66432 rows x 4096 x 2048  905 / 1015    16 groups, 34688 rows x 2048 x 4096  495 / 546
+//     64 groups, 73600 rows x 4096 x 2048  1029 / 1126  32 weight gradients of 4096 x 2048  699 / 713
+//     but 16 weight gradients of 2048 x 2048  202 / 185: a tile's stores weigh more with nine steps;
+//     3000 x 8192 x 5120, which takes 128x128, 238 / 240, and 2560 rows 236 / 206
 hipError_t launch_fp8_matmul(const Fp8Matmul &p, hipStream_t s) {
-  const bool few = p.mode == kDense ? p.m <= 32 : p.mode == kGroupedRows && p.m <= 24 * static_cast<uint64_t>(p.groups);
+  const bool few = p.mode == kDense ? p.m <= 32 : p.mode == kGroupedRows && p.m <= 32 * static_cast<uint64_t>(p.groups);
   if (few) {
     // a wave's share is best at least the four blocks that it asks for at once
     if (p.kblocks >= 24) return launch_rows<8>(p, s);

@@ -77,3 +77,10 @@ def test_weight_gradients(m, n, out):
     d, va, vb, off = nv.fp8_matmul_grouped_k(a, b, plan, out_dtype=out), F.values(a), F.values(b), H.i64(plan.offsets)
     for e in range(6):
         F.check_product(d[e], va[:, off[e]:off[e + 1]], vb[:, off[e]:off[e + 1]])
+
+
+# the average that still takes the few-row kernel, and the next one
+@pytest.mark.parametrize("counts", [[32] * 8, [40, 24, 32, 31, 33, 31, 64, 1], [33] * 8])
+@pytest.mark.parametrize("out", OUT)
+def test_groups_around_the_few_row_limit(counts, out):
+    check_groups(counts, 1, 200, 1700, out)
