@@ -14,7 +14,7 @@ P = 0x100000  # a fake, aligned device address
     ((1 << 31) - 1, 1, 1),    # 2^24 tiles of 128 rows, 256 threads each
     ((1 << 31) - 1, 1, 0),    # the same where only zeros are written
     (1, (1 << 31) - 1, 1),    # few rows: 2^26 tiles of 32 columns, one wave each
-    (32, 1 << 28, 24 * 128),  # few rows, eight waves each
+    (32, 1 << 28, 26 * 128),  # few rows, eight waves each
 ])
 @pytest.mark.parametrize("b_2d", [0, 1])
 def test_dense(m, n, k, b_2d):
