@@ -28,7 +28,7 @@ namespace {
 constexpr uint32_t kWave = 64;
 
 // ---------------------------------------------------------------------------
-// Sort: a counting sort over at most kMaxExperts keys. A workgroup of 16
+// Sort: a counting sort over at most kMaxKeys keys. A workgroup of 16
 // waves takes a chunk of slots; inside it each wave takes consecutive slots,
 // 64 at a time, and ranks them by matching keys across its lanes (eight
 // ballots, one for each bit of the key), so ranks follow the slots' order

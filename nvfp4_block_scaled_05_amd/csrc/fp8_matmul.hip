@@ -22,10 +22,11 @@
 // a multiply-add with b's, and that first product may.) The tile kernels therefore
 // look at the scales that they use (near()), and where that could be, the wave
 // computes its part of the tile again, by add_far(), which multiplies mantissas and
-// adds exponents. Looking costs 2 to 4% up to 512 rows and 1 to 2% above (512 x 4096 x
-// 4096 22.3 -> 22.7 us, 8192 x 8192 x 5120 498 -> 503); a product whose every tile is
-// computed again takes ten times as long. The few-row kernel, which has time beside
-// its loads, always takes add_far().
+// adds exponents. Looking costs 1% in 256x256 tiles with 128x128 blocks of b (8192 x
+// 8192 x 5120 498 -> 503 us) and 2 to 5% elsewhere (512 x 4096 x 4096 22.1 -> 22.7, 32
+// weight gradients of 4096 x 2048 664 -> 680); a product whose every tile is computed
+// again takes ten times as long. The few-row kernel, which has time beside its loads,
+// always takes add_far().
 #include "codec.h"
 #include "launch.h"
 
@@ -238,7 +239,7 @@ __device__ __forceinline__ f32x4 add_far(f32x4 acc, f32x4 c, float sa, f32x4 sb)
 // KS times as many waves may share a tile, each share with every KS-th block,
 // stages and accumulators of its own, which are added up at the end.
 //
-// At 8192 x 8192 x 5120 this takes 570 to 600 us (1.2 PFLOP/s, by the box) in
+// At 8192 x 8192 x 5120 this takes 580 to 607 us (1.15 PFLOP/s, by the box) in
 // 128x128 tiles, two workgroups a CU. The widening and the scaling are 3 vector
 // instructions for each v_mfma; measured alone, a v_mfma takes 17 cycles with up
 // to two of them beside it and 22 with three, and the mix of this kernel from
@@ -251,8 +252,8 @@ __device__ __forceinline__ f32x4 add_far(f32x4 acc, f32x4 c, float sa, f32x4 sb)
 // wait, then read and widen b, and leave the matrix cores idle together: 570
 // us. So the two waves of each SIMD run half a step apart. Waves 0 .. 3 (upper
 // half of the rows) begin a step at one barrier and pass the next one in the
-// middle of it, where waves 4 .. 7 begin theirs: 535 to 545 us, and 492 to 510 us
-// (1.35 to 1.40 PFLOP/s) with the instructions in groups, below.
+// middle of it, where waves 4 .. 7 begin theirs: 535 to 545 us, and 484 to 516 us
+// (1.33 to 1.42 PFLOP/s) with the instructions in groups, below.
 // What that needs of the two stages: each half of the waves loads its own rows
 // of a, at its own steps' beginnings; b is read at a step's beginning only, so
 // the stage that the lower half has read by the middle of its step k, which is
@@ -269,7 +270,7 @@ __device__ __forceinline__ f32x4 add_far(f32x4 acc, f32x4 c, float sa, f32x4 sb)
 // + r of a group of 16 G as its rows 4 q + r, so that a lane ends with 4 G
 // consecutive columns of d: 16 bytes, which four lanes continue to 64. (With
 // G 4 a store is 16 bytes of every 64; the FP32 weight gradients of 32 groups,
-// 4096 x 2048 each, took 780 us so, and take 711.)
+// 4096 x 2048 each, took 780 us so, and took 711 in the same tiles without.)
 // ---------------------------------------------------------------------------
 // f(r) of b: with that order of its rows, eight lanes that follow each other get eight values
 template <uint32_t G>
