@@ -520,6 +520,70 @@ nvfp4_status_t nvfp4_fp8_matmul_grouped_k(const nvfp4_fp8_t *a, const nvfp4_fp8_
                                           int64_t groups, int64_t m, int64_t n, int64_t k, void *d,
                                           nvfp4_dtype_t d_dtype, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * MXFP4: E2M1 values with a power of two for each 32 of them, the 4-bit form
+ * that the matrix cores multiply as it is. Conventions as for the FP8 calls.
+ * ------------------------------------------------------------------------- */
+
+/* An MXFP4 matrix of n rows of k values.
+ *   data   E2M1 codes, two a byte, the even element in the low half:
+ *          [n][nvfp4_fp8_pitch(k) / 2]; codes k .. of a row are zero. 16-byte
+ *          aligned.
+ *   scales E8M0 bytes s, a scale of 2^(s - 127) (255: NaN) for each 32 values
+ *          of a row, four for each 128: [ceil(k / 128)][n][4]. 4-byte aligned.
+ * A batch has its matrices one after the other in both arrays. */
+typedef struct {
+  uint8_t *data;
+  uint8_t *scales;
+} nvfp4_mxfp4_t;
+
+/*
+ * Quantize a batch of matrices x [batch][rows][cols] to MXFP4; arguments,
+ * orientations and row_slots as in nvfp4_fp8_quantize. block_2d 0: a scale for
+ * 32 values along each orientation's rows; 1: for 32 x 32 values (of rows and
+ * columns that are multiples of 32 on), so that both orientations hold the same
+ * values; each row of a block then has the byte.
+ * Per block: m = max|v|, s = max(floor(log2 m) + 127 - 2, 0) (0 for m = 0), code
+ * = E2M1(v / 2^(s - 127)), nearest even, at most 6 in magnitude. The rows and
+ * columns that a block lacks count as zeros. A block with an infinity or a NaN
+ * has scale 255 and zero codes: all of it decodes to NaN.
+ */
+nvfp4_status_t nvfp4_mxfp4_quantize(const void *x, nvfp4_dtype_t dtype, int64_t batch, int64_t rows, int64_t cols,
+                                    const int32_t *row_slots, int64_t tokens, int64_t topk, uint32_t block_2d,
+                                    const nvfp4_mxfp4_t *row, const nvfp4_mxfp4_t *col, void *stream);
+
+/*
+ * The values y [batch][n][k] of a batch of MXFP4 matrices, FP32 or BF16 (exact in
+ * both, but for those of scales 253 and 254 that are past their largest
+ * number: infinities). y is 16-byte aligned.
+ */
+nvfp4_status_t nvfp4_mxfp4_dequantize(const nvfp4_mxfp4_t *q, int64_t batch, int64_t n, int64_t k, void *y,
+                                      nvfp4_dtype_t y_dtype, void *stream);
+
+/*
+ * d = a b^T: a has m rows of k values, b has n rows of k values, d is [m][n] of
+ * d_dtype, 16-byte aligned. Any m, n; k < 2^23; k = 0 gives zeros. Orientations
+ * as in nvfp4_fp8_matmul. Scales may be any; a sum that leaves FP32's range on
+ * the way is an infinity or NaN. Outputs too large for one launch are refused
+ * as a shape.
+ */
+nvfp4_status_t nvfp4_mxfp4_matmul(const nvfp4_mxfp4_t *a, const nvfp4_mxfp4_t *b, int64_t m, int64_t n, int64_t k, void *d,
+                                  nvfp4_dtype_t d_dtype, void *stream);
+
+/* The experts' products, as nvfp4_fp8_matmul_grouped: rows offsets[g] ..
+ * offsets[g + 1] - 1 of a times matrix g of the batch b [groups]; rows from
+ * offsets[groups] on are set to zero. */
+nvfp4_status_t nvfp4_mxfp4_matmul_grouped(const nvfp4_mxfp4_t *a, const nvfp4_mxfp4_t *b, const int32_t *offsets,
+                                          int64_t groups, int64_t rows, int64_t n, int64_t k, void *d,
+                                          nvfp4_dtype_t d_dtype, void *stream);
+
+/* The experts' weight gradients, as nvfp4_fp8_matmul_grouped_k: for each group g,
+ * d[g] [m][n] = a b^T over columns offsets[g] .. offsets[g + 1] - 1 of both;
+ * offsets are multiples of 128. */
+nvfp4_status_t nvfp4_mxfp4_matmul_grouped_k(const nvfp4_mxfp4_t *a, const nvfp4_mxfp4_t *b, const int32_t *offsets,
+                                            int64_t groups, int64_t m, int64_t n, int64_t k, void *d,
+                                            nvfp4_dtype_t d_dtype, void *stream);
+
 /* Text for the last non-OK status returned on the calling thread ("" when
  * none). The pointer stays valid until the next call on that thread. */
 const char *nvfp4_last_error(void);

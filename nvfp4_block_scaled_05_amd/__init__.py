@@ -58,7 +58,9 @@ EXPORTED = ("nvfp4_compute_amax", "nvfp4_quantize", "nvfp4_dequantize", "nvfp4_l
             "nvfp4_quantize_noalloc", "nvfp4_debug_set_rht_unit", "nvfp4_debug_set_resident_variant",
             "nvfp4_expert_rows", "nvfp4_expert_sort_workspace_bytes", "nvfp4_expert_sort", "nvfp4_expert_gather",
             "nvfp4_expert_combine", "nvfp4_expert_combine_grad", "nvfp4_fp8_pitch", "nvfp4_fp8_quantize",
-            "nvfp4_fp8_matmul", "nvfp4_fp8_matmul_grouped", "nvfp4_fp8_matmul_grouped_k")
+            "nvfp4_fp8_matmul", "nvfp4_fp8_matmul_grouped", "nvfp4_fp8_matmul_grouped_k",
+            "nvfp4_mxfp4_quantize", "nvfp4_mxfp4_dequantize", "nvfp4_mxfp4_matmul", "nvfp4_mxfp4_matmul_grouped",
+            "nvfp4_mxfp4_matmul_grouped_k")
 
 
 class nvfp4_out_t(ctypes.Structure):
@@ -66,6 +68,10 @@ class nvfp4_out_t(ctypes.Structure):
 
 
 class nvfp4_fp8_t(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class nvfp4_mxfp4_t(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
 
 
@@ -169,6 +175,17 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
     lib.nvfp4_fp8_matmul_grouped.argtypes = [FP8, FP8, P, I64, I64, I64, I64, P, I, P]
     lib.nvfp4_fp8_matmul_grouped_k.restype = I
     lib.nvfp4_fp8_matmul_grouped_k.argtypes = [FP8, FP8, P, I64, I64, I64, I64, P, I, P]
+    MX = ctypes.POINTER(nvfp4_mxfp4_t)
+    lib.nvfp4_mxfp4_quantize.restype = I
+    lib.nvfp4_mxfp4_quantize.argtypes = [P, I, I64, I64, I64, P, I64, I64, U32, MX, MX, P]
+    lib.nvfp4_mxfp4_dequantize.restype = I
+    lib.nvfp4_mxfp4_dequantize.argtypes = [MX, I64, I64, I64, P, I, P]
+    lib.nvfp4_mxfp4_matmul.restype = I
+    lib.nvfp4_mxfp4_matmul.argtypes = [MX, MX, I64, I64, I64, P, I, P]
+    lib.nvfp4_mxfp4_matmul_grouped.restype = I
+    lib.nvfp4_mxfp4_matmul_grouped.argtypes = [MX, MX, P, I64, I64, I64, I64, P, I, P]
+    lib.nvfp4_mxfp4_matmul_grouped_k.restype = I
+    lib.nvfp4_mxfp4_matmul_grouped_k.argtypes = [MX, MX, P, I64, I64, I64, I64, P, I, P]
     _lib = lib
     return lib
 
@@ -695,24 +712,30 @@ def _blocks(n: int) -> int:
     return (n + FP8_BLOCK - 1) // FP8_BLOCK
 
 
+def _matrices(x: torch.Tensor, plan: Optional[ExpertPlan]):
+    """What a quantize call takes x [R][C] or [B][R][C] for, or x [tokens][C] with a plan: its
+    device, leading shape, matrices, their rows and columns, and the plan's row_slots, tokens and topk."""
+    dev = _on(x, "x")
+    if x.dim() != 2 and (x.dim() != 3 or plan is not None):
+        raise ValueError("x must be [R][C] or, without a plan, [B][R][C]")
+    lead, batch = tuple(x.shape[:-2]), x.shape[0] if x.dim() == 3 else 1
+    rows, cols = x.shape[-2:]
+    if plan is None:
+        return dev, lead, batch, rows, cols, None, 0, 1
+    _want_plan(plan, dev)
+    if rows != plan.tokens:
+        raise ValueError(f"x must be [{plan.tokens}][cols], got {tuple(x.shape)}")
+    return dev, lead, batch, plan.rows, cols, plan.row_slots, plan.tokens, plan.topk
+
+
 def fp8_quantize(x: torch.Tensor, *, rowwise=True, columnwise=False, block_2d=False, plan: Optional[ExpertPlan] = None,
                  stream=None):
     """Quantize x [R][C], or a batch [B][R][C], to block-scaled FP8 (1x128
     blocks, or 128x128 with block_2d). Returns (row, col): x itself with k = C,
     and its transpose with k = R; None for one not asked for. With a plan, x
     is [tokens][C] and the matrix is expert_gather(x, plan)."""
-    dev = _on(x, "x")
-    if x.dim() != 2 and (x.dim() != 3 or plan is not None):
-        raise ValueError("x must be [R][C] or, without a plan, [B][R][C]")
+    dev, lead, batch, rows, cols, slots, tokens, topk = _matrices(x, plan)
     code = _dtype_code(x)
-    lead, batch = tuple(x.shape[:-2]), x.shape[0] if x.dim() == 3 else 1
-    rows, cols = x.shape[-2:]
-    slots, tokens, topk = None, 0, 1
-    if plan is not None:
-        _want_plan(plan, dev)
-        if rows != plan.tokens:
-            raise ValueError(f"x must be [{plan.tokens}][cols], got {tuple(x.shape)}")
-        slots, tokens, topk, rows = plan.row_slots, plan.tokens, plan.topk, plan.rows
     if (context := _elsewhere(stream, dev)) is not None:
         with context:
             return fp8_quantize(x, rowwise=rowwise, columnwise=columnwise, block_2d=block_2d, plan=plan)
@@ -793,4 +816,120 @@ def fp8_matmul_grouped_k(a: Fp8Tensor, b: Fp8Tensor, plan: ExpertPlan, *, out_dt
     d = torch.empty((plan.experts, a.n, b.n), dtype=out_dtype, device=dev)
     _check(load().nvfp4_fp8_matmul_grouped_k(a.as_c(), b.as_c(), plan.offsets.data_ptr(), plan.experts, a.n, b.n, plan.rows,
                                              d.data_ptr(), code, _current(dev)))
+    return d
+
+
+# ---- MXFP4: quantization and back, products -----------------------------------
+
+@dataclasses.dataclass
+class Mxfp4Tensor:
+    """n rows of k values in MXFP4, or a batch of such matrices.
+
+    data uint8 [..][n][pitch(k) / 2], two E2M1 codes a byte (the even element in
+    the low half), zero from k on; scales uint8 [..][ceil(k / 128)][n][4], an E8M0
+    byte for each 32 values of a row."""
+    data: torch.Tensor
+    scales: torch.Tensor
+    n: int
+    k: int
+
+    def as_c(self) -> nvfp4_mxfp4_t:
+        return nvfp4_mxfp4_t(self.data.data_ptr(), self.scales.data_ptr())
+
+
+def mxfp4_quantize(x: torch.Tensor, *, rowwise=True, columnwise=False, block_2d=False, plan: Optional[ExpertPlan] = None,
+                   stream=None):
+    """Quantize x [R][C], or a batch [B][R][C], to MXFP4 (a scale for 32 values
+    of a row, or with block_2d for 32x32). Returns (row, col): x itself with k =
+    C, and its transpose with k = R; None for one not asked for. With a plan, x
+    is [tokens][C] and the matrix is expert_gather(x, plan)."""
+    dev, lead, batch, rows, cols, slots, tokens, topk = _matrices(x, plan)
+    code = _dtype_code(x)
+    if (context := _elsewhere(stream, dev)) is not None:
+        with context:
+            return mxfp4_quantize(x, rowwise=rowwise, columnwise=columnwise, block_2d=block_2d, plan=plan)
+
+    def empty(n, k):
+        return Mxfp4Tensor(torch.empty((*lead, n, _blocks(k) * (FP8_BLOCK // 2)), dtype=torch.uint8, device=dev),
+                           torch.empty((*lead, _blocks(k), n, 4), dtype=torch.uint8, device=dev), n, k)
+
+    row = empty(rows, cols) if rowwise else None
+    col = empty(cols, rows) if columnwise else None
+    r, c = row.as_c() if row is not None else None, col.as_c() if col is not None else None
+    _check(load().nvfp4_mxfp4_quantize(x.data_ptr(), code, batch, rows, cols, _ptr(slots), tokens, topk, int(block_2d), r, c, _current(dev)))
+    return row, col
+
+
+def _want_mxfp4(q: Mxfp4Tensor, lead, n: int, k: int, device, what: str) -> None:
+    if q.n != n or q.k != k:
+        raise ValueError(f"{what} must have {n} rows of {k} values, got {q.n} x {q.k}")
+    kb = (k + FP8_BLOCK - 1) // FP8_BLOCK
+    _want(q.data, torch.uint8, (*lead, n, kb * (FP8_BLOCK // 2)), device, what)
+    _want(q.scales, torch.uint8, (*lead, kb, n, 4), device, what)
+
+
+def mxfp4_dequantize(q: Mxfp4Tensor, *, out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    """The values of q, [n][k] or [B][n][k]; bfloat16 and float32 hold them exactly."""
+    dev = _on(q.data, "the tensor")
+    code = _out_code(out_dtype)
+    lead = tuple(q.data.shape[:-2])
+    if len(lead) > 1:
+        raise ValueError(f"the tensor must be one matrix or a batch of them, got {tuple(q.data.shape)}")
+    _want_mxfp4(q, lead, q.n, q.k, dev, "the tensor")
+    if (context := _elsewhere(stream, dev)) is not None:
+        with context:
+            return mxfp4_dequantize(q, out_dtype=out_dtype)
+    y = torch.empty((*lead, q.n, q.k), dtype=out_dtype, device=dev)
+    _check(load().nvfp4_mxfp4_dequantize(q.as_c(), lead[0] if lead else 1, q.n, q.k, y.data_ptr(), code, _current(dev)))
+    return y
+
+
+def mxfp4_matmul(a: Mxfp4Tensor, b: Mxfp4Tensor, *, out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    """a b^T [a.n][b.n]."""
+    dev = _on(a.data, "operand a")
+    code = _out_code(out_dtype)
+    _want_mxfp4(a, (), a.n, a.k, dev, "operand a")
+    _want_mxfp4(b, (), b.n, a.k, dev, "operand b")
+    if (context := _elsewhere(stream, dev)) is not None:
+        with context:
+            return mxfp4_matmul(a, b, out_dtype=out_dtype)
+    d = torch.empty((a.n, b.n), dtype=out_dtype, device=dev)
+    _check(load().nvfp4_mxfp4_matmul(a.as_c(), b.as_c(), a.n, b.n, a.k, d.data_ptr(), code, _current(dev)))
+    return d
+
+
+def mxfp4_matmul_grouped(a: Mxfp4Tensor, b: Mxfp4Tensor, plan: ExpertPlan, *, out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    """Each expert's rows of a (plan.rows rows) times its matrix of the batch b
+    ([experts]): [plan.rows][b.n], zeros past the last expert's rows."""
+    dev = _on(a.data, "operand a")
+    code = _out_code(out_dtype)
+    _want_plan(plan, dev)
+    _want_mxfp4(a, (), plan.rows, a.k, dev, "operand a")
+    _want_mxfp4(b, (plan.experts,), b.n, a.k, dev, "operand b")
+    if (context := _elsewhere(stream, dev)) is not None:
+        with context:
+            return mxfp4_matmul_grouped(a, b, plan, out_dtype=out_dtype)
+    d = torch.empty((plan.rows, b.n), dtype=out_dtype, device=dev)
+    _check(load().nvfp4_mxfp4_matmul_grouped(a.as_c(), b.as_c(), plan.offsets.data_ptr(), plan.experts, plan.rows, b.n, a.k,
+                                             d.data_ptr(), code, _current(dev)))
+    return d
+
+
+def mxfp4_matmul_grouped_k(a: Mxfp4Tensor, b: Mxfp4Tensor, plan: ExpertPlan, *, out_dtype=torch.float32, stream=None) -> torch.Tensor:
+    """Per expert, a b^T over its rows, which are k here: [experts][a.n][b.n],
+    zeros for an expert without rows. a and b are column-wise orientations of
+    sorted rows (k = plan.rows) and the plan's align is 128."""
+    dev = _on(a.data, "operand a")
+    code = _out_code(out_dtype)
+    _want_plan(plan, dev)
+    if plan.align != FP8_BLOCK:
+        raise ValueError(f"the plan must be aligned to {FP8_BLOCK} rows, got {plan.align}")
+    _want_mxfp4(a, (), a.n, plan.rows, dev, "operand a")
+    _want_mxfp4(b, (), b.n, plan.rows, dev, "operand b")
+    if (context := _elsewhere(stream, dev)) is not None:
+        with context:
+            return mxfp4_matmul_grouped_k(a, b, plan, out_dtype=out_dtype)
+    d = torch.empty((plan.experts, a.n, b.n), dtype=out_dtype, device=dev)
+    _check(load().nvfp4_mxfp4_matmul_grouped_k(a.as_c(), b.as_c(), plan.offsets.data_ptr(), plan.experts, a.n, b.n, plan.rows,
+                                               d.data_ptr(), code, _current(dev)))
     return d

@@ -612,15 +612,18 @@ nvfp4_status_t check_rows(nvfp4_dtype_t dtype, int64_t tokens, int64_t topk, int
   return NVFP4_OK;
 }
 
-nvfp4_status_t check_fp8(const nvfp4_fp8_t *q, bool empty, const char *what) {
+// An operand of two arrays: codes and scales.
+template <typename T>
+nvfp4_status_t check_operand(const T *q, bool empty, const char *what) {
   if (q == nullptr) return fail(NVFP4_ERR_NULL, "%s is NULL", what);
   nvfp4_status_t st = check_buffer(q->data, 16, empty, what);
   return st != NVFP4_OK ? st : check_buffer(q->scales, 4, empty, what);
 }
 
-// The checks that the three products share, and their launch. rows: of a.
-nvfp4_status_t matmul(const nvfp4_fp8_t *a, const nvfp4_fp8_t *b, int64_t rows, int64_t n, int64_t k, bool b_block_2d,
-                      uint32_t mode, const int32_t *offsets, int64_t groups, void *d, nvfp4_dtype_t d_dtype, void *stream) {
+// The checks that the products share. rows: of a; done: there is nothing to compute.
+template <typename T>
+nvfp4_status_t check_matmul(const T *a, const T *b, int64_t rows, int64_t n, int64_t k, uint32_t mode, const int32_t *offsets,
+                            int64_t groups, const void *d, nvfp4_dtype_t d_dtype, bool *done) {
   nvfp4_status_t st = check_dtype(d_dtype, "output");
   if (st != NVFP4_OK) return st;
   if (rows < 0 || n < 0 || k < 0 || rows >= kIndexLimit || n >= kIndexLimit)
@@ -632,11 +635,26 @@ nvfp4_status_t matmul(const nvfp4_fp8_t *a, const nvfp4_fp8_t *b, int64_t rows, 
   if (product_at_least(row_tiles, ceil_div(n, 16), kIndexLimit))
     return fail(NVFP4_ERR_SHAPE, "an output of %lld x %lld is too large for one launch", (long long)rows, (long long)n);
   const bool empty = rows == 0 || n == 0;
-  if ((st = check_fp8(a, empty || k == 0, "operand a")) != NVFP4_OK) return st;
-  if ((st = check_fp8(b, empty || k == 0, "operand b")) != NVFP4_OK) return st;
+  if ((st = check_operand(a, empty || k == 0, "operand a")) != NVFP4_OK) return st;
+  if ((st = check_operand(b, empty || k == 0, "operand b")) != NVFP4_OK) return st;
   if ((st = check_buffer(d, 16, empty, "the output")) != NVFP4_OK) return st;
   if (mode != nvfp4::kDense && (st = check_buffer(offsets, 4, false, "offsets")) != NVFP4_OK) return st;
-  if (empty) return NVFP4_OK;
+  *done = empty;
+  return NVFP4_OK;
+}
+
+// A product's launch, which refuses grids that are too large.
+nvfp4_status_t matmul_status(hipError_t e, int64_t rows, int64_t n, const char *what) {
+  if (e == hipErrorInvalidConfiguration)
+    return fail(NVFP4_ERR_SHAPE, "an output of %lld x %lld is too large for one launch", (long long)rows, (long long)n);
+  return hip_status(e, what);
+}
+
+nvfp4_status_t matmul(const nvfp4_fp8_t *a, const nvfp4_fp8_t *b, int64_t rows, int64_t n, int64_t k, bool b_block_2d,
+                      uint32_t mode, const int32_t *offsets, int64_t groups, void *d, nvfp4_dtype_t d_dtype, void *stream) {
+  bool done = false;
+  const nvfp4_status_t st = check_matmul(a, b, rows, n, k, mode, offsets, groups, d, d_dtype, &done);
+  if (st != NVFP4_OK || done) return st;
   nvfp4::Fp8Matmul p{};
   p.a = a->data;
   p.sa = a->scales;
@@ -653,10 +671,47 @@ nvfp4_status_t matmul(const nvfp4_fp8_t *a, const nvfp4_fp8_t *b, int64_t rows, 
   p.mode = mode;
   p.offsets = offsets;
   p.groups = static_cast<uint32_t>(groups);
-  const hipError_t e = nvfp4::launch_fp8_matmul(p, static_cast<hipStream_t>(stream));
-  if (e == hipErrorInvalidConfiguration)
-    return fail(NVFP4_ERR_SHAPE, "an output of %lld x %lld is too large for one launch", (long long)rows, (long long)n);
-  return hip_status(e, "FP8 product launch");
+  return matmul_status(nvfp4::launch_fp8_matmul(p, static_cast<hipStream_t>(stream)), rows, n, "FP8 product launch");
+}
+
+nvfp4_status_t matmul(const nvfp4_mxfp4_t *a, const nvfp4_mxfp4_t *b, int64_t rows, int64_t n, int64_t k, uint32_t mode,
+                      const int32_t *offsets, int64_t groups, void *d, nvfp4_dtype_t d_dtype, void *stream) {
+  bool done = false;
+  const nvfp4_status_t st = check_matmul(a, b, rows, n, k, mode, offsets, groups, d, d_dtype, &done);
+  if (st != NVFP4_OK || done) return st;
+  nvfp4::Mxfp4Matmul p{};
+  p.a = a->data;
+  p.sa = reinterpret_cast<const uint32_t *>(a->scales);
+  p.b = b->data;
+  p.sb = reinterpret_cast<const uint32_t *>(b->scales);
+  p.d = d;
+  p.m = static_cast<uint32_t>(rows);
+  p.n = static_cast<uint32_t>(n);
+  p.kblocks = static_cast<uint32_t>(ceil_div(k, nvfp4::kFp8Block));
+  p.out_fp32 = d_dtype == NVFP4_IN_FP32;
+  p.mode = mode;
+  p.offsets = offsets;
+  p.groups = static_cast<uint32_t>(groups);
+  return matmul_status(nvfp4::launch_mxfp4_matmul(p, static_cast<hipStream_t>(stream)), rows, n, "MXFP4 product launch");
+}
+
+// The shapes and maps of a quantize call by tiles of 128 x 128.
+nvfp4_status_t check_tiles(const void *x, nvfp4_dtype_t dtype, int64_t batch, int64_t rows, int64_t cols, const int32_t *row_slots,
+                           int64_t tokens, int64_t topk, const void *row, const void *col) {
+  nvfp4_status_t st = check_dtype(dtype, "input");
+  if (st != NVFP4_OK) return st;
+  if (batch < 0 || rows < 0 || cols < 0 || batch >= kIndexLimit || rows >= kIndexLimit || cols >= kIndexLimit)
+    return fail(NVFP4_ERR_SHAPE, "a batch of %lld matrices of %lld x %lld", (long long)batch, (long long)rows, (long long)cols);
+  const int64_t tiles = ceil_div(rows, nvfp4::kFp8Block) * ceil_div(cols, nvfp4::kFp8Block);
+  if (product_at_least(tiles, batch, kIndexLimit)) return fail(NVFP4_ERR_SHAPE, "2^31 or more blocks of 128 x 128");
+  if (row == nullptr && col == nullptr) return fail(NVFP4_ERR_NULL, "neither a row-wise nor a column-wise output");
+  if (row_slots != nullptr) {
+    if (batch != 1) return fail(NVFP4_ERR_UNSUPPORTED, "row_slots takes a batch of one matrix");
+    if (!aligned(row_slots, 4)) return fail(NVFP4_ERR_ALIGN, "row_slots is not 4-byte aligned");
+    if ((st = check_slots(tokens, topk)) != NVFP4_OK) return st;
+  }
+  const bool empty = batch == 0 || rows == 0 || cols == 0;
+  return check_buffer(x, 16, empty || (row_slots && tokens == 0), "x");
 }
 
 }  // namespace
@@ -785,22 +840,11 @@ extern "C" uint64_t nvfp4_fp8_pitch(int64_t k) {
 extern "C" nvfp4_status_t nvfp4_fp8_quantize(const void *x, nvfp4_dtype_t dtype, int64_t batch, int64_t rows, int64_t cols,
                                              const int32_t *row_slots, int64_t tokens, int64_t topk, uint32_t block_2d,
                                              const nvfp4_fp8_t *row, const nvfp4_fp8_t *col, void *stream) {
-  nvfp4_status_t st = check_dtype(dtype, "input");
+  nvfp4_status_t st = check_tiles(x, dtype, batch, rows, cols, row_slots, tokens, topk, row, col);
   if (st != NVFP4_OK) return st;
-  if (batch < 0 || rows < 0 || cols < 0 || batch >= kIndexLimit || rows >= kIndexLimit || cols >= kIndexLimit)
-    return fail(NVFP4_ERR_SHAPE, "a batch of %lld matrices of %lld x %lld", (long long)batch, (long long)rows, (long long)cols);
-  const int64_t tiles = ceil_div(rows, nvfp4::kFp8Block) * ceil_div(cols, nvfp4::kFp8Block);
-  if (product_at_least(tiles, batch, kIndexLimit)) return fail(NVFP4_ERR_SHAPE, "2^31 or more blocks of 128 x 128");
-  if (row == nullptr && col == nullptr) return fail(NVFP4_ERR_NULL, "neither a row-wise nor a column-wise output");
-  if (row_slots != nullptr) {
-    if (batch != 1) return fail(NVFP4_ERR_UNSUPPORTED, "row_slots takes a batch of one matrix");
-    if (!aligned(row_slots, 4)) return fail(NVFP4_ERR_ALIGN, "row_slots is not 4-byte aligned");
-    if ((st = check_slots(tokens, topk)) != NVFP4_OK) return st;
-  }
-  const bool empty = batch * rows * cols == 0;
-  if ((st = check_buffer(x, 16, empty || (row_slots && tokens == 0), "x")) != NVFP4_OK) return st;
-  if (row && (st = check_fp8(row, empty, "the row-wise output")) != NVFP4_OK) return st;
-  if (col && (st = check_fp8(col, empty, "the column-wise output")) != NVFP4_OK) return st;
+  const bool empty = batch == 0 || rows == 0 || cols == 0;
+  if (row && (st = check_operand(row, empty, "the row-wise output")) != NVFP4_OK) return st;
+  if (col && (st = check_operand(col, empty, "the column-wise output")) != NVFP4_OK) return st;
   if (empty) return NVFP4_OK;
   nvfp4::Fp8Quantize p{};
   p.x = x;
@@ -833,4 +877,63 @@ extern "C" nvfp4_status_t nvfp4_fp8_matmul_grouped_k(const nvfp4_fp8_t *a, const
                                                      int64_t groups, int64_t m, int64_t n, int64_t k, void *d,
                                                      nvfp4_dtype_t d_dtype, void *stream) {
   return matmul(a, b, m, n, k, false, nvfp4::kGroupedK, offsets, groups, d, d_dtype, stream);
+}
+
+extern "C" nvfp4_status_t nvfp4_mxfp4_quantize(const void *x, nvfp4_dtype_t dtype, int64_t batch, int64_t rows, int64_t cols,
+                                               const int32_t *row_slots, int64_t tokens, int64_t topk, uint32_t block_2d,
+                                               const nvfp4_mxfp4_t *row, const nvfp4_mxfp4_t *col, void *stream) {
+  nvfp4_status_t st = check_tiles(x, dtype, batch, rows, cols, row_slots, tokens, topk, row, col);
+  if (st != NVFP4_OK) return st;
+  const bool empty = batch == 0 || rows == 0 || cols == 0;
+  if (row && (st = check_operand(row, empty, "the row-wise output")) != NVFP4_OK) return st;
+  if (col && (st = check_operand(col, empty, "the column-wise output")) != NVFP4_OK) return st;
+  if (empty) return NVFP4_OK;
+  nvfp4::Mxfp4Quantize p{};
+  p.x = x;
+  p.batch = static_cast<uint32_t>(batch);
+  p.rows = static_cast<uint32_t>(rows);
+  p.cols = static_cast<uint32_t>(cols);
+  p.row_slots = row_slots;
+  p.slots = row_slots ? static_cast<uint32_t>(tokens * topk) : 0;
+  p.topk = row_slots ? static_cast<uint32_t>(topk) : 1;
+  p.row_data = row ? row->data : nullptr;
+  p.row_scales = row ? row->scales : nullptr;
+  p.col_data = col ? col->data : nullptr;
+  p.col_scales = col ? col->scales : nullptr;
+  return hip_status(nvfp4::launch_mxfp4_quantize(p, dtype, block_2d != 0, static_cast<hipStream_t>(stream)),
+                    "MXFP4 quantize launch");
+}
+
+extern "C" nvfp4_status_t nvfp4_mxfp4_dequantize(const nvfp4_mxfp4_t *q, int64_t batch, int64_t n, int64_t k, void *y,
+                                                 nvfp4_dtype_t y_dtype, void *stream) {
+  nvfp4_status_t st = check_dtype(y_dtype, "output");
+  if (st != NVFP4_OK) return st;
+  if (batch < 0 || n < 0 || k < 0 || batch >= kIndexLimit || n >= kIndexLimit || k >= kIndexLimit)
+    return fail(NVFP4_ERR_SHAPE, "a batch of %lld matrices of %lld x %lld", (long long)batch, (long long)n, (long long)k);
+  if (product_at_least(ceil_div(n, nvfp4::kFp8Block) * ceil_div(k, nvfp4::kFp8Block), batch, kIndexLimit))
+    return fail(NVFP4_ERR_SHAPE, "2^31 or more blocks of 128 x 128");
+  const bool empty = batch == 0 || n == 0 || k == 0;
+  if ((st = check_operand(q, empty, "the tensor")) != NVFP4_OK) return st;
+  if ((st = check_buffer(y, 16, empty, "the output")) != NVFP4_OK) return st;
+  if (empty) return NVFP4_OK;
+  return hip_status(nvfp4::launch_mxfp4_dequantize(q->data, q->scales, static_cast<uint32_t>(batch), static_cast<uint32_t>(n),
+                                                   static_cast<uint32_t>(k), y_dtype == NVFP4_IN_FP32, y, static_cast<hipStream_t>(stream)),
+                    "MXFP4 dequantize launch");
+}
+
+extern "C" nvfp4_status_t nvfp4_mxfp4_matmul(const nvfp4_mxfp4_t *a, const nvfp4_mxfp4_t *b, int64_t m, int64_t n, int64_t k, void *d,
+                                             nvfp4_dtype_t d_dtype, void *stream) {
+  return matmul(a, b, m, n, k, nvfp4::kDense, nullptr, 0, d, d_dtype, stream);
+}
+
+extern "C" nvfp4_status_t nvfp4_mxfp4_matmul_grouped(const nvfp4_mxfp4_t *a, const nvfp4_mxfp4_t *b, const int32_t *offsets,
+                                                     int64_t groups, int64_t rows, int64_t n, int64_t k, void *d,
+                                                     nvfp4_dtype_t d_dtype, void *stream) {
+  return matmul(a, b, rows, n, k, nvfp4::kGroupedRows, offsets, groups, d, d_dtype, stream);
+}
+
+extern "C" nvfp4_status_t nvfp4_mxfp4_matmul_grouped_k(const nvfp4_mxfp4_t *a, const nvfp4_mxfp4_t *b, const int32_t *offsets,
+                                                       int64_t groups, int64_t m, int64_t n, int64_t k, void *d,
+                                                       nvfp4_dtype_t d_dtype, void *stream) {
+  return matmul(a, b, m, n, k, nvfp4::kGroupedK, offsets, groups, d, d_dtype, stream);
 }

@@ -258,6 +258,35 @@ struct Fp8Matmul {
   uint32_t groups;
 };
 hipError_t launch_fp8_matmul(const Fp8Matmul &p, hipStream_t s);
+
+// MXFP4: rows of codes padded as FP8's, two codes a byte, and four scale bytes
+// for each kFp8Block values of a row, [kblocks][n][4].
+struct Mxfp4Quantize {
+  const void *x;  // as Fp8Quantize's
+  uint32_t batch, rows, cols;
+  const int32_t *row_slots;
+  uint32_t slots, topk;
+  uint8_t *row_data, *col_data;  // NULL: orientation not written
+  uint8_t *row_scales, *col_scales;
+};
+hipError_t launch_mxfp4_quantize(const Mxfp4Quantize &p, int dtype, bool block_2d, hipStream_t s);
+// y [batch][n][k] in FP32 or BF16; nothing is empty
+hipError_t launch_mxfp4_dequantize(const uint8_t *data, const uint8_t *scales, uint32_t batch, uint32_t n, uint32_t k, bool out_fp32, void *y,
+                                   hipStream_t s);
+
+// d = a b^T; modes as above. Scales are words of four, [kblocks][rows].
+struct Mxfp4Matmul {
+  const uint8_t *a, *b;
+  const uint32_t *sa, *sb;
+  void *d;
+  uint32_t m, n, kblocks;  // as Fp8Matmul's
+  bool out_fp32;
+  uint32_t mode;
+  const int32_t *offsets;  // device, [groups + 1]
+  uint32_t groups;
+};
+hipError_t launch_mxfp4_matmul(const Mxfp4Matmul &p, hipStream_t s);
+
 hipError_t launch_debug_e2m1(const float *v, const uint32_t *r, uint8_t *out, uint64_t n, bool sr, bool pairwise,
                              hipStream_t s);
 hipError_t launch_debug_rht(const void *x, int dtype, uint32_t rows, uint32_t cols, uint32_t mask, float *t,

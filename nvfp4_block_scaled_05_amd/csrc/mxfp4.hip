@@ -1,0 +1,252 @@
+// MXFP4: E2M1 codes with one E8M0 scale (a power of two) for each 32 values
+// along a row (or each 32x32), in the row-wise and the column-wise (transposed)
+// orientation from one read of the input, and the way back.
+//
+//   m = max|v| of the block, E its exponent field in binary32
+//   s = max(E - 2, 0); 255 (NaN) where E is 255, an infinity or a NaN
+//   X = 2^(s - 127); code = E2M1(v / X), nearest even, at most 6; 0 where s is 255
+//
+// which is 2^(floor(log2 m) - 2), clamped at 2^-127: |v / X| < 8, and what is
+// above 6 becomes 6. v / X is v times a power of two and exact, unless it
+// is below 2^-126, where the code is 0 anyway.
+//
+// One workgroup per 128x128 tile, in registers: thread t holds the 8x8 patch
+// at rows 8 (t / 16), columns 8 (t % 16). Four neighbouring lanes hold a row's
+// block of 32 and a wave holds 32 rows, so every maximum stays inside a wave.
+// A patch's 8 codes of a row (of a column) are one word; the words pass
+// through LDS so that they leave 16 bytes a lane, 64 contiguous bytes a row.
+// Columns and rows past the end count as zeros; each orientation's rows are
+// padded to a multiple of 128 with zero codes, which every tile writes whole.
+#include "codec.h"
+#include "launch.h"
+#include "patch.h"
+
+namespace nvfp4 {
+namespace {
+
+constexpr uint32_t kThreads = 256;
+constexpr uint32_t kTile = kFp8Block;
+constexpr uint32_t kPerWord = kTile / 8;  // words of a tile's row of codes
+
+struct Args {
+  const void *x;
+  uint32_t rows, cols;             // of one matrix
+  uint32_t row_tiles, col_tiles;
+  uint32_t tiles;                  // of all matrices
+  const int32_t *row_slots;
+  uint32_t slots, topk;
+  uint8_t *row_data, *col_data;
+  uint32_t *row_scales, *col_scales;  // four blocks a word
+};
+
+// The scale byte of a block from its largest magnitude's bits.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits) {
+  const uint32_t e = amax_bits >> 23;
+  return e == 255 ? 255 : e > 2 ? e - 2 : 0;
+}
+// 1 / X; 0 for the NaN scale, whose infinities and NaN encode() then drops.
+__device__ __forceinline__ float inverse(uint32_t s) { return __uint_as_float((254 - s) << 23); }
+
+// Eight values of a block with scale byte s.
+__device__ __forceinline__ uint32_t encode(const float *v, uint32_t s) {
+  const float e = inverse(s);
+  float t[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) t[i] = v[i] * e;
+  const uint32_t w = e2m1_rne_x8(t);
+  return s == 255 ? 0 : w;
+}
+
+// Where the word of row i and column group g of a tile is: eight rows take 16
+// words more than they fill, and groups of four words are swapped by pairs of eights,
+// so that a wave's 16 column groups of four rows, and its four row groups of
+// 16 columns of the transposed tile, meet every bank twice, which 64 lanes must.
+constexpr uint32_t kEight = 9 * kPerWord;
+__device__ __forceinline__ uint32_t place(uint32_t i, uint32_t g) { return i / 8 * kEight + i % 8 * kPerWord + (g ^ (i / 16 % 4 * 4)); }
+
+template <int DT, bool BLOCK_2D>
+__global__ __launch_bounds__(kThreads) void k_mxfp4_quantize(Args a) {
+  __shared__ __attribute__((aligned(16))) uint32_t straight[kTile / 8 * kEight], turned[kTile / 8 * kEight];
+  __shared__ __attribute__((aligned(4))) uint8_t col_bytes[kTile][4];
+  const uint32_t t = threadIdx.x, cg = t % 16, rg = t / 16, lane = t % 64, wave = t / 64;
+  const uint32_t block = block_of_long_grid();
+  if (block >= a.tiles) return;
+  const uint32_t per_batch = a.row_tiles * a.col_tiles, batch = block / per_batch, id = block - batch * per_batch;
+  uint32_t ct = id % a.col_tiles, rt = id / a.col_tiles;
+  if (a.row_slots != nullptr) {
+    // a token's row is read topk times: an XCD (workgroups go to the eight in
+    // turn) takes whole strips of 128 columns, so that its L2 keeps them
+    const uint32_t strip = id / (8 * a.row_tiles) * 8, in = id - strip * a.row_tiles, wide = min(8u, a.col_tiles - strip);
+    ct = strip + in % wide;
+    rt = in / wide;
+  }
+  const uint32_t r0 = rt * kTile, c0 = ct * kTile;
+  const uint32_t c = c0 + 8 * cg;
+  const uint32_t left = c < a.cols ? a.cols - c : 0;
+
+  Patch<DT> v;
+#pragma unroll
+  for (uint32_t p = 0; p < 8; ++p) {
+    const uint32_t r = r0 + 8 * rg + p;
+    bool have = r < a.rows && left > 0;
+    uint64_t src = static_cast<uint64_t>(batch) * a.rows + r;
+    if (a.row_slots != nullptr && have) {
+      const uint32_t slot = static_cast<uint32_t>(a.row_slots[r]);
+      have = slot < a.slots;
+      src = slot / a.topk;
+    }
+    if (have) v.load(p, a.x, src * a.cols + c, left);
+    else v.clear(p);
+  }
+
+  const bool want_row = a.row_data != nullptr, want_col = a.col_data != nullptr;
+  uint32_t col_max[8];
+  if (BLOCK_2D || want_col) v.col_max(col_max);  // over the wave's 32 rows
+  uint32_t both = 0;
+  if (BLOCK_2D) {
+    uint32_t m = col_max[0];
+#pragma unroll
+    for (int q = 1; q < 8; ++q) m = max(m, col_max[q]);
+    m = max(m, dpp_mov<kQuadXor1>(m));
+    both = scale_byte(max(m, dpp_mov<kQuadXor2>(m)));
+  }
+
+  if (want_row) {
+    uint32_t mine = 0;  // the scale word of row cg of the patch
+#pragma unroll
+    for (uint32_t p = 0; p < 8; ++p) {
+      uint32_t s = both;
+      if (!BLOCK_2D) {
+        uint32_t m = v.row_max(p);
+        m = max(m, dpp_mov<kQuadXor1>(m));
+        s = scale_byte(max(m, dpp_mov<kQuadXor2>(m)));
+      }
+      uint32_t w = s << (8 * (cg / 4));  // the row's four blocks: the other quads', by mirrors
+      w |= dpp_mov<0x141>(w);
+      w |= dpp_mov<0x140>(w);
+      mine = cg == p ? w : mine;
+      float f[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) f[q] = v.get(p, q);
+      straight[place(8 * rg + p, cg)] = encode(f, s);
+    }
+    const uint32_t r = r0 + 8 * rg + cg;
+    if (cg < 8 && r < a.rows) a.row_scales[(static_cast<uint64_t>(batch) * a.col_tiles + ct) * a.rows + r] = mine;
+  }
+  if (want_col) {
+#pragma unroll
+    for (uint32_t q = 0; q < 8; ++q) {
+      const uint32_t s = BLOCK_2D ? both : scale_byte(col_max[q]);
+      float f[8];
+#pragma unroll
+      for (int p = 0; p < 8; ++p) f[p] = v.get(p, q);
+      turned[place(8 * cg + q, rg)] = encode(f, s);
+      if (lane < 16) col_bytes[8 * cg + q][wave] = static_cast<uint8_t>(s);
+    }
+  }
+  __syncthreads();
+
+  const uint32_t piece = t % 4;  // 16 bytes of a row of the tile
+  const u32x4 *const from[2] = {reinterpret_cast<const u32x4 *>(straight), reinterpret_cast<const u32x4 *>(turned)};
+#pragma unroll
+  for (uint32_t side = 0; side < 2; ++side) {
+    uint8_t *const data = side == 0 ? a.row_data : a.col_data;
+    if (data == nullptr) continue;
+    const uint32_t n = side == 0 ? a.rows : a.cols, n0 = side == 0 ? r0 : c0, kt = side == 0 ? ct : rt;
+    const uint64_t pitch = static_cast<uint64_t>(side == 0 ? a.col_tiles : a.row_tiles) * (kTile / 2);
+    uint8_t *const dst = data + (static_cast<uint64_t>(batch) * n + n0) * pitch + kt * (kTile / 2) + 16 * piece;
+#pragma unroll
+    for (uint32_t h = 0; h < 2; ++h) {
+      const uint32_t i = t / 4 + 64 * h;
+      if (n0 + i < n) *reinterpret_cast<u32x4 *>(dst + i * pitch) = from[side][place(i, 4 * piece) / 4];
+    }
+  }
+  if (want_col && t < kTile && c0 + t < a.cols)
+    a.col_scales[(static_cast<uint64_t>(batch) * a.row_tiles + rt) * a.cols + c0 + t] = *reinterpret_cast<const uint32_t *>(col_bytes[t]);
+}
+
+// ---------------------------------------------------------------------------
+// The values: y [n][k] of code * X, exact in binary32 and BF16 both. One
+// thread per 16 values, 8 bytes of codes.
+// ---------------------------------------------------------------------------
+struct BackArgs {
+  const uint8_t *data, *scales;
+  void *y;
+  uint32_t n, k, kblocks;
+  uint32_t per_row;  // threads that a row takes
+  uint64_t units;    // rows of all matrices times per_row
+};
+
+template <bool OUT32>
+__global__ __launch_bounds__(kThreads) void k_mxfp4_dequantize(BackArgs a) {
+  const uint64_t unit = static_cast<uint64_t>(block_of_long_grid()) * kThreads + threadIdx.x;
+  if (unit >= a.units) return;
+  const uint64_t row = unit / a.per_row;
+  const uint32_t at = static_cast<uint32_t>(unit - row * a.per_row) * 16;  // the first of its values
+  const uint64_t batch = row / a.n;
+  const uint32_t r = static_cast<uint32_t>(row - batch * a.n);
+  const u32x2 w = *reinterpret_cast<const u32x2 *>(a.data + row * (static_cast<uint64_t>(a.kblocks) * (kFp8Block / 2)) + at / 2);
+  const uint32_t s = a.scales[((batch * a.kblocks + at / kFp8Block) * a.n + r) * 4 + at / 32 % 4];
+  // 2^(s - 127), which is subnormal for 0; NaN for 255
+  const float x = __uint_as_float(s == 0 ? 0x00400000u : s == 255 ? 0x7FC00000u : s << 23);
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  float v[16];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const f2 p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[h], 1.0f, 0), p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[h], 1.0f, 1);
+    const f2 p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[h], 1.0f, 2), p3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[h], 1.0f, 3);
+    v[8 * h + 0] = p0.x * x, v[8 * h + 1] = p0.y * x, v[8 * h + 2] = p1.x * x, v[8 * h + 3] = p1.y * x;
+    v[8 * h + 4] = p2.x * x, v[8 * h + 5] = p2.y * x, v[8 * h + 6] = p3.x * x, v[8 * h + 7] = p3.y * x;
+  }
+  const uint64_t to = row * a.k + at;
+  if (at + 16 <= a.k) {
+    if (OUT32) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<u32x4_any *>(static_cast<float *>(a.y) + to + 4 * i) =
+            u32x4_any{__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])};
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        *reinterpret_cast<u32x4_any *>(static_cast<uint16_t *>(a.y) + to + 8 * i) =
+            u32x4_any{bf16_pair(v[8 * i], v[8 * i + 1]), bf16_pair(v[8 * i + 2], v[8 * i + 3]), bf16_pair(v[8 * i + 4], v[8 * i + 5]),
+                      bf16_pair(v[8 * i + 6], v[8 * i + 7])};
+    }
+    return;
+  }
+#pragma unroll
+  for (uint32_t i = 0; i < 16; ++i) {
+    if (at + i >= a.k) continue;
+    if (OUT32) static_cast<float *>(a.y)[to + i] = v[i];
+    else static_cast<uint16_t *>(a.y)[to + i] = static_cast<uint16_t>(bf16_pair(v[i], 0.0f));
+  }
+}
+
+template <int DT, bool BLOCK_2D>
+hipError_t launch(const Args &a, hipStream_t s) {
+  if (a.tiles == 0) return hipSuccess;
+  hipLaunchKernelGGL((k_mxfp4_quantize<DT, BLOCK_2D>), long_grid(a.tiles), dim3(kThreads), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_mxfp4_quantize(const Mxfp4Quantize &p, int dtype, bool block_2d, hipStream_t s) {
+  const uint32_t row_tiles = (p.rows + kTile - 1) / kTile, col_tiles = (p.cols + kTile - 1) / kTile;
+  const Args a{p.x, p.rows, p.cols, row_tiles, col_tiles, p.batch * row_tiles * col_tiles, p.row_slots, p.slots, p.topk,
+               p.row_data, p.col_data, reinterpret_cast<uint32_t *>(p.row_scales), reinterpret_cast<uint32_t *>(p.col_scales)};
+  if (dtype == kBF16) return block_2d ? launch<kBF16, true>(a, s) : launch<kBF16, false>(a, s);
+  return block_2d ? launch<kFP32, true>(a, s) : launch<kFP32, false>(a, s);
+}
+
+hipError_t launch_mxfp4_dequantize(const uint8_t *data, const uint8_t *scales, uint32_t batch, uint32_t n, uint32_t k, bool out_fp32, void *y,
+                                   hipStream_t s) {
+  BackArgs a{data, scales, y, n, k, (k + kFp8Block - 1) / kFp8Block, (k + 15) / 16, 0};
+  a.units = static_cast<uint64_t>(batch) * n * a.per_row;
+  const dim3 grid = long_grid((a.units + kThreads - 1) / kThreads);
+  if (out_fp32) hipLaunchKernelGGL((k_mxfp4_dequantize<true>), grid, dim3(kThreads), 0, s, a);
+  else hipLaunchKernelGGL((k_mxfp4_dequantize<false>), grid, dim3(kThreads), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace nvfp4
