@@ -584,6 +584,37 @@ nvfp4_status_t nvfp4_mxfp4_matmul_grouped_k(const nvfp4_mxfp4_t *a, const nvfp4_
                                             int64_t groups, int64_t m, int64_t n, int64_t k, void *d,
                                             nvfp4_dtype_t d_dtype, void *stream);
 
+/* Most slots (tokens * topk) of the expert layer for a few tokens. */
+#define NVFP4_EXPERT_MLP_MAX_SLOTS 1024
+
+/* Bytes of nvfp4_expert_mlp_*'s workspace (0 for arguments that they refuse). */
+uint64_t nvfp4_expert_mlp_workspace_bytes(int64_t tokens, int64_t topk, int64_t hidden);
+
+/*
+ * An expert layer for a few tokens (a decoding step), in two launches:
+ *   out[t] = sum over j of weights[t][j] w2[e] act(w1[e] x[t]), e = ids[t][j]
+ * ids [tokens][topk] as in nvfp4_expert_sort (an id outside 0 .. experts - 1
+ * leaves its choice out; an expert that a token names twice counts twice),
+ * weights FP32 [tokens][topk]. gated 1: w1[e] has 2 hidden rows of cols values
+ * and act(g, u) = silu(g) u of its first and second half; 0: hidden rows and act =
+ * silu. w2[e] has cols rows of hidden values. w1 and w2 are batches of `experts`
+ * matrices, MXFP4 or FP8 in 128x128 blocks. x and out are BF16 [tokens][cols],
+ * 16-byte aligned, any cols and hidden from 1 to 2^23 - 1. Sums are held in FP32;
+ * act's results are rounded to BF16. Only the experts that ids names are read.
+ * tokens * topk at most NVFP4_EXPERT_MLP_MAX_SLOTS, experts in 1 ..
+ * NVFP4_MAX_GROUPS. workspace: 16-byte aligned, at least
+ * nvfp4_expert_mlp_workspace_bytes(); its contents do not matter, and calls that
+ * may overlap need one each. The same bits every time.
+ */
+nvfp4_status_t nvfp4_expert_mlp_mxfp4(const void *x, int64_t tokens, int64_t cols, const void *ids, uint32_t id_bytes,
+                                      const float *weights, int64_t topk, int64_t experts, const nvfp4_mxfp4_t *w1,
+                                      const nvfp4_mxfp4_t *w2, int64_t hidden, uint32_t gated, void *workspace, void *out,
+                                      void *stream);
+nvfp4_status_t nvfp4_expert_mlp_fp8(const void *x, int64_t tokens, int64_t cols, const void *ids, uint32_t id_bytes,
+                                    const float *weights, int64_t topk, int64_t experts, const nvfp4_fp8_t *w1,
+                                    const nvfp4_fp8_t *w2, int64_t hidden, uint32_t gated, void *workspace, void *out,
+                                    void *stream);
+
 /* Text for the last non-OK status returned on the calling thread ("" when
  * none). The pointer stays valid until the next call on that thread. */
 const char *nvfp4_last_error(void);

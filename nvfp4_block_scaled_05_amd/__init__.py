@@ -51,6 +51,7 @@ NVFP4_DEBUG_SR = 1
 NVFP4_DEBUG_PAIRWISE = 2
 
 NVFP4_MAX_GROUPS = 256
+NVFP4_EXPERT_MLP_MAX_SLOTS = 1024
 
 EXPORTED = ("nvfp4_compute_amax", "nvfp4_quantize", "nvfp4_dequantize", "nvfp4_last_error",
             "nvfp4_workspace_bytes", "nvfp4_swizzle_scales", "nvfp4_swizzled_scales_bytes", "nvfp4_quantize_grouped",
@@ -60,7 +61,7 @@ EXPORTED = ("nvfp4_compute_amax", "nvfp4_quantize", "nvfp4_dequantize", "nvfp4_l
             "nvfp4_expert_combine", "nvfp4_expert_combine_grad", "nvfp4_fp8_pitch", "nvfp4_fp8_quantize",
             "nvfp4_fp8_matmul", "nvfp4_fp8_matmul_grouped", "nvfp4_fp8_matmul_grouped_k",
             "nvfp4_mxfp4_quantize", "nvfp4_mxfp4_dequantize", "nvfp4_mxfp4_matmul", "nvfp4_mxfp4_matmul_grouped",
-            "nvfp4_mxfp4_matmul_grouped_k")
+            "nvfp4_mxfp4_matmul_grouped_k", "nvfp4_expert_mlp_workspace_bytes", "nvfp4_expert_mlp_mxfp4", "nvfp4_expert_mlp_fp8")
 
 
 class nvfp4_out_t(ctypes.Structure):
@@ -186,6 +187,12 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
     lib.nvfp4_mxfp4_matmul_grouped.argtypes = [MX, MX, P, I64, I64, I64, I64, P, I, P]
     lib.nvfp4_mxfp4_matmul_grouped_k.restype = I
     lib.nvfp4_mxfp4_matmul_grouped_k.argtypes = [MX, MX, P, I64, I64, I64, I64, P, I, P]
+    lib.nvfp4_expert_mlp_workspace_bytes.restype = ctypes.c_uint64
+    lib.nvfp4_expert_mlp_workspace_bytes.argtypes = [I64, I64, I64]
+    lib.nvfp4_expert_mlp_mxfp4.restype = I
+    lib.nvfp4_expert_mlp_mxfp4.argtypes = [P, I64, I64, P, U32, P, I64, I64, MX, MX, I64, U32, P, P, P]
+    lib.nvfp4_expert_mlp_fp8.restype = I
+    lib.nvfp4_expert_mlp_fp8.argtypes = [P, I64, I64, P, U32, P, I64, I64, FP8, FP8, I64, U32, P, P, P]
     _lib = lib
     return lib
 
@@ -933,3 +940,48 @@ def mxfp4_matmul_grouped_k(a: Mxfp4Tensor, b: Mxfp4Tensor, plan: ExpertPlan, *, 
     _check(load().nvfp4_mxfp4_matmul_grouped_k(a.as_c(), b.as_c(), plan.offsets.data_ptr(), plan.experts, a.n, b.n, plan.rows,
                                                d.data_ptr(), code, _current(dev)))
     return d
+
+
+# ---- an expert layer for a few tokens -----------------------------------------
+
+def expert_mlp(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w1, w2, *, gated=True, stream=None) -> torch.Tensor:
+    """An expert layer for a decoding step, in two launches: out[t] = the sum over
+    j of weights[t][j] w2[e] act(w1[e] x[t]) with e = ids[t][j], [tokens][cols] bfloat16.
+
+    x bfloat16 [tokens][cols]; ids int32 or int64 [tokens][topk] (an id outside 0
+    .. experts - 1 leaves its choice out); weights float32 [tokens][topk]; tokens *
+    topk at most 1024. w1 is a batch [experts] with k = cols and n = 2 hidden, act
+    = silu of the first half's products times the second half's, or (not gated) n =
+    hidden and act = silu; w2 has n = cols and k = hidden. Both are Mxfp4Tensors
+    or both Fp8Tensors in 128x128 blocks. Larger batches go through expert_sort
+    and the grouped products."""
+    dev = _on(x, "x")
+    if x.dim() != 2 or x.dtype is not torch.bfloat16:
+        raise ValueError(f"x must be bfloat16 [tokens][cols], got {x.dtype} {tuple(x.shape)}")
+    tokens, cols = x.shape
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2 or ids.dtype not in (torch.int32, torch.int64):
+        raise ValueError("ids must be int32 or int64 [tokens][topk]")
+    topk = ids.shape[1]
+    _want(ids, ids.dtype, (tokens, topk), dev, "ids")
+    _want(weights, torch.float32, (tokens, topk), dev, "weights")
+    if isinstance(w1, Fp8Tensor) != isinstance(w2, Fp8Tensor):
+        raise ValueError("w1 and w2 must have one format")
+    hidden, experts = w2.k, w2.data.shape[0]
+    n1 = 2 * hidden if gated else hidden
+    lib = load()
+    if isinstance(w1, Fp8Tensor):
+        _want_fp8(w1, (experts,), n1, cols, True, dev, "w1")
+        _want_fp8(w2, (experts,), cols, hidden, True, dev, "w2")
+        call = lib.nvfp4_expert_mlp_fp8
+    else:
+        _want_mxfp4(w1, (experts,), n1, cols, dev, "w1")
+        _want_mxfp4(w2, (experts,), cols, hidden, dev, "w2")
+        call = lib.nvfp4_expert_mlp_mxfp4
+    if (context := _elsewhere(stream, dev)) is not None:
+        with context:
+            return expert_mlp(x, ids, weights, w1, w2, gated=gated)
+    out = torch.empty_like(x)
+    workspace = torch.empty((lib.nvfp4_expert_mlp_workspace_bytes(tokens, topk, hidden),), dtype=torch.uint8, device=dev)
+    _check(call(x.data_ptr(), tokens, cols, ids.data_ptr(), ids.element_size(), weights.data_ptr(), topk, experts, w1.as_c(), w2.as_c(),
+                hidden, int(gated), workspace.data_ptr(), out.data_ptr(), _current(dev)))
+    return out

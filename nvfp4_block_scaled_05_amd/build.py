@@ -27,7 +27,8 @@ LIB = os.path.join(HERE, "libnvfp4.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["api.cpp", "amax.hip", "cast.hip", "rowscaled.hip", "dequant.hip", "swizzle.hip", "hooks.hip",
-           "experts.hip", "fp8.hip", "fp8_matmul.hip", "mxfp4.hip", "mxfp4_matmul.hip"]
+           "experts.hip", "fp8.hip", "fp8_matmul.hip", "mxfp4.hip", "mxfp4_matmul.hip",
+           "expert_mlp.hip"]
 ARCH = "gfx950"
 
 COMMON = [

@@ -937,3 +937,75 @@ extern "C" nvfp4_status_t nvfp4_mxfp4_matmul_grouped_k(const nvfp4_mxfp4_t *a, c
                                                        nvfp4_dtype_t d_dtype, void *stream) {
   return matmul(a, b, m, n, k, nvfp4::kGroupedK, offsets, groups, d, d_dtype, stream);
 }
+
+namespace {
+
+nvfp4_status_t check_mlp(int64_t tokens, int64_t topk, int64_t experts, int64_t cols, int64_t hidden) {
+  nvfp4_status_t st = check_sort(tokens, topk, experts, 1);
+  if (st != NVFP4_OK) return st;
+  if (tokens * topk > NVFP4_EXPERT_MLP_MAX_SLOTS)
+    return fail(NVFP4_ERR_SHAPE, "tokens * topk = %lld must be at most %d", (long long)(tokens * topk), NVFP4_EXPERT_MLP_MAX_SLOTS);
+  if (cols < 1 || cols >= kFp8KLimit || hidden < 1 || hidden >= kFp8KLimit)
+    return fail(NVFP4_ERR_SHAPE, "cols = %lld and hidden = %lld must be in [1, 2^23)", (long long)cols, (long long)hidden);
+  return NVFP4_OK;
+}
+
+template <typename T>
+nvfp4_status_t expert_mlp(const void *x, int64_t tokens, int64_t cols, const void *ids, uint32_t id_bytes, const float *weights,
+                          int64_t topk, int64_t experts, const T *w1, const T *w2, int64_t hidden, uint32_t gated, void *workspace,
+                          void *out, void *stream, bool fp8) {
+  nvfp4_status_t st = check_mlp(tokens, topk, experts, cols, hidden);
+  if (st != NVFP4_OK) return st;
+  if (id_bytes != 4 && id_bytes != 8) return fail(NVFP4_ERR_UNSUPPORTED, "ids of %u bytes", id_bytes);
+  const bool none = tokens == 0;
+  if ((st = check_buffer(x, 16, none, "x")) != NVFP4_OK) return st;
+  if ((st = check_buffer(ids, id_bytes, none, "ids")) != NVFP4_OK) return st;
+  if ((st = check_buffer(weights, 4, none, "weights")) != NVFP4_OK) return st;
+  if ((st = check_operand(w1, none, "w1")) != NVFP4_OK) return st;
+  if ((st = check_operand(w2, none, "w2")) != NVFP4_OK) return st;
+  if ((st = check_buffer(workspace, 16, none, "the workspace")) != NVFP4_OK) return st;
+  if ((st = check_buffer(out, 16, none, "the output")) != NVFP4_OK) return st;
+  if (none) return NVFP4_OK;
+  nvfp4::ExpertMlp p{};
+  p.x = x;
+  p.ids = ids;
+  p.wide = id_bytes == 8;
+  p.weights = weights;
+  p.w1 = w1->data;
+  p.s1 = w1->scales;
+  p.w2 = w2->data;
+  p.s2 = w2->scales;
+  p.fp8 = fp8;
+  p.gated = gated != 0;
+  p.workspace = static_cast<uint32_t *>(workspace);
+  p.out = out;
+  p.tokens = static_cast<uint32_t>(tokens);
+  p.topk = static_cast<uint32_t>(topk);
+  p.experts = static_cast<uint32_t>(experts);
+  p.cols = static_cast<uint32_t>(cols);
+  p.hidden = static_cast<uint32_t>(hidden);
+  const hipError_t e = nvfp4::launch_expert_mlp(p, static_cast<hipStream_t>(stream));
+  if (e == hipErrorInvalidConfiguration) return fail(NVFP4_ERR_SHAPE, "hidden = %lld is too large for one launch", (long long)hidden);
+  return hip_status(e, "expert layer launch");
+}
+
+}  // namespace
+
+extern "C" uint64_t nvfp4_expert_mlp_workspace_bytes(int64_t tokens, int64_t topk, int64_t hidden) {
+  if (check_mlp(tokens, topk, 1, 1, hidden) != NVFP4_OK) return 0;
+  return nvfp4::expert_mlp_workspace_bytes(static_cast<uint64_t>(tokens * topk), static_cast<uint64_t>(hidden));
+}
+
+extern "C" nvfp4_status_t nvfp4_expert_mlp_mxfp4(const void *x, int64_t tokens, int64_t cols, const void *ids, uint32_t id_bytes,
+                                                 const float *weights, int64_t topk, int64_t experts, const nvfp4_mxfp4_t *w1,
+                                                 const nvfp4_mxfp4_t *w2, int64_t hidden, uint32_t gated, void *workspace, void *out,
+                                                 void *stream) {
+  return expert_mlp(x, tokens, cols, ids, id_bytes, weights, topk, experts, w1, w2, hidden, gated, workspace, out, stream, false);
+}
+
+extern "C" nvfp4_status_t nvfp4_expert_mlp_fp8(const void *x, int64_t tokens, int64_t cols, const void *ids, uint32_t id_bytes,
+                                               const float *weights, int64_t topk, int64_t experts, const nvfp4_fp8_t *w1,
+                                               const nvfp4_fp8_t *w2, int64_t hidden, uint32_t gated, void *workspace, void *out,
+                                               void *stream) {
+  return expert_mlp(x, tokens, cols, ids, id_bytes, weights, topk, experts, w1, w2, hidden, gated, workspace, out, stream, true);
+}

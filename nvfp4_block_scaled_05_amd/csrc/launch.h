@@ -287,6 +287,24 @@ struct Mxfp4Matmul {
 };
 hipError_t launch_mxfp4_matmul(const Mxfp4Matmul &p, hipStream_t s);
 
+// The expert layer for a few tokens; nothing is empty but the dropped slots.
+constexpr uint32_t kMlpMaxSlots = 1024;
+constexpr uint32_t kMlpHeader = (1 + 3 * kMaxGroups + 3 + kMlpMaxSlots) * 4;
+struct ExpertMlp {
+  const void *x;  // BF16 [tokens][cols]
+  const void *ids;
+  uint32_t wide;  // 64-bit ids
+  const float *weights;
+  const uint8_t *w1, *w2;  // [experts][hidden or 2 hidden][pitch(cols)], [experts][cols][pitch(hidden)]
+  const void *s1, *s2;
+  bool fp8, gated;  // MXFP4 weights or FP8 ones
+  uint32_t *workspace;
+  void *out;  // BF16 [tokens][cols]
+  uint32_t tokens, topk, experts, cols, hidden;
+};
+uint64_t expert_mlp_workspace_bytes(uint64_t slots, uint64_t hidden);
+hipError_t launch_expert_mlp(const ExpertMlp &p, hipStream_t s);
+
 hipError_t launch_debug_e2m1(const float *v, const uint32_t *r, uint8_t *out, uint64_t n, bool sr, bool pairwise,
                              hipStream_t s);
 hipError_t launch_debug_rht(const void *x, int dtype, uint32_t rows, uint32_t cols, uint32_t mask, float *t,
