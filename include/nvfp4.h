@@ -588,10 +588,10 @@ nvfp4_status_t nvfp4_mxfp4_matmul_grouped_k(const nvfp4_mxfp4_t *a, const nvfp4_
 #define NVFP4_EXPERT_MLP_MAX_SLOTS 1024
 
 /* Bytes of nvfp4_expert_mlp_*'s workspace (0 for arguments that they refuse). */
-uint64_t nvfp4_expert_mlp_workspace_bytes(int64_t tokens, int64_t topk, int64_t hidden);
+uint64_t nvfp4_expert_mlp_workspace_bytes(int64_t tokens, int64_t topk, int64_t cols, int64_t hidden);
 
 /*
- * An expert layer for a few tokens (a decoding step), in two launches:
+ * An expert layer for a few tokens (a decoding step), in three launches:
  *   out[t] = sum over j of weights[t][j] w2[e] act(w1[e] x[t]), e = ids[t][j]
  * ids [tokens][topk] as in nvfp4_expert_sort (an id outside 0 .. experts - 1
  * leaves its choice out; an expert that a token names twice counts twice),
@@ -599,8 +599,8 @@ uint64_t nvfp4_expert_mlp_workspace_bytes(int64_t tokens, int64_t topk, int64_t 
  * and act(g, u) = silu(g) u of its first and second half; 0: hidden rows and act =
  * silu. w2[e] has cols rows of hidden values. w1 and w2 are batches of `experts`
  * matrices, MXFP4 or FP8 in 128x128 blocks. x and out are BF16 [tokens][cols],
- * 16-byte aligned, any cols and hidden from 1 to 2^23 - 1. Sums are held in FP32;
- * act's results are rounded to BF16. Only the experts that ids names are read.
+ * 16-byte aligned, any cols and hidden from 1 to 2^23 - 1. Sums are held in FP32,
+ * act's results in 16 bits of mantissa. Only the experts that ids names are read.
  * tokens * topk at most NVFP4_EXPERT_MLP_MAX_SLOTS, experts in 1 ..
  * NVFP4_MAX_GROUPS. workspace: 16-byte aligned, at least
  * nvfp4_expert_mlp_workspace_bytes(); its contents do not matter, and calls that

@@ -188,7 +188,7 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
     lib.nvfp4_mxfp4_matmul_grouped_k.restype = I
     lib.nvfp4_mxfp4_matmul_grouped_k.argtypes = [MX, MX, P, I64, I64, I64, I64, P, I, P]
     lib.nvfp4_expert_mlp_workspace_bytes.restype = ctypes.c_uint64
-    lib.nvfp4_expert_mlp_workspace_bytes.argtypes = [I64, I64, I64]
+    lib.nvfp4_expert_mlp_workspace_bytes.argtypes = [I64, I64, I64, I64]
     lib.nvfp4_expert_mlp_mxfp4.restype = I
     lib.nvfp4_expert_mlp_mxfp4.argtypes = [P, I64, I64, P, U32, P, I64, I64, MX, MX, I64, U32, P, P, P]
     lib.nvfp4_expert_mlp_fp8.restype = I
@@ -945,7 +945,7 @@ def mxfp4_matmul_grouped_k(a: Mxfp4Tensor, b: Mxfp4Tensor, plan: ExpertPlan, *, 
 # ---- an expert layer for a few tokens -----------------------------------------
 
 def expert_mlp(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w1, w2, *, gated=True, stream=None) -> torch.Tensor:
-    """An expert layer for a decoding step, in two launches: out[t] = the sum over
+    """An expert layer for a decoding step, in three launches: out[t] = the sum over
     j of weights[t][j] w2[e] act(w1[e] x[t]) with e = ids[t][j], [tokens][cols] bfloat16.
 
     x bfloat16 [tokens][cols]; ids int32 or int64 [tokens][topk] (an id outside 0
@@ -981,7 +981,7 @@ def expert_mlp(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w1, w2
         with context:
             return expert_mlp(x, ids, weights, w1, w2, gated=gated)
     out = torch.empty_like(x)
-    workspace = torch.empty((lib.nvfp4_expert_mlp_workspace_bytes(tokens, topk, hidden),), dtype=torch.uint8, device=dev)
+    workspace = torch.empty((lib.nvfp4_expert_mlp_workspace_bytes(tokens, topk, cols, hidden),), dtype=torch.uint8, device=dev)
     _check(call(x.data_ptr(), tokens, cols, ids.data_ptr(), ids.element_size(), weights.data_ptr(), topk, experts, w1.as_c(), w2.as_c(),
                 hidden, int(gated), workspace.data_ptr(), out.data_ptr(), _current(dev)))
     return out

@@ -984,16 +984,14 @@ nvfp4_status_t expert_mlp(const void *x, int64_t tokens, int64_t cols, const voi
   p.experts = static_cast<uint32_t>(experts);
   p.cols = static_cast<uint32_t>(cols);
   p.hidden = static_cast<uint32_t>(hidden);
-  const hipError_t e = nvfp4::launch_expert_mlp(p, static_cast<hipStream_t>(stream));
-  if (e == hipErrorInvalidConfiguration) return fail(NVFP4_ERR_SHAPE, "hidden = %lld is too large for one launch", (long long)hidden);
-  return hip_status(e, "expert layer launch");
+  return hip_status(nvfp4::launch_expert_mlp(p, static_cast<hipStream_t>(stream)), "expert layer launch");
 }
 
 }  // namespace
 
-extern "C" uint64_t nvfp4_expert_mlp_workspace_bytes(int64_t tokens, int64_t topk, int64_t hidden) {
-  if (check_mlp(tokens, topk, 1, 1, hidden) != NVFP4_OK) return 0;
-  return nvfp4::expert_mlp_workspace_bytes(static_cast<uint64_t>(tokens * topk), static_cast<uint64_t>(hidden));
+extern "C" uint64_t nvfp4_expert_mlp_workspace_bytes(int64_t tokens, int64_t topk, int64_t cols, int64_t hidden) {
+  if (check_mlp(tokens, topk, 1, cols, hidden) != NVFP4_OK) return 0;
+  return nvfp4::expert_mlp_workspace_bytes(static_cast<uint64_t>(tokens * topk), static_cast<uint64_t>(cols), static_cast<uint64_t>(hidden));
 }
 
 extern "C" nvfp4_status_t nvfp4_expert_mlp_mxfp4(const void *x, int64_t tokens, int64_t cols, const void *ids, uint32_t id_bytes,

@@ -1,21 +1,31 @@
-// A whole expert layer for a few tokens, in two launches:
+// A whole expert layer for a few tokens, in three launches:
 //
 //   h[s] = act(w1[e] x[t])            for each slot s = t topk + j with expert e = ids[t][j]
-//   out[t] = sum over j of weights[t][j] w2[e] h[s]
+//   y[s] = w2[e] h[s]
+//   out[t] = sum over j of weights[t][j] y[s]
 //
 // act(g, u) = silu(g) u for the two halves of w1's rows, or silu(g); weights in
 // MXFP4 or block-scaled FP8 (128x128 blocks), x and out BF16. Bound by reading
 // the weights of the experts in use, once each; so the codes are widened to BF16
 // in registers (exact: E2M1 values times a power of two, and E4M3 values, are
 // BF16 values) and multiplied by v_mfma_f32_16x16x32_bf16, which sums to binary32,
-// and no activation is quantized. h is rounded to BF16 on its way to the second
-// kernel, which reads all of it in every workgroup: half the bytes and
-// products of FP32, for an error below that of out's own rounding.
+// and no activation is quantized. h goes from the first kernel to the second as
+// two BF16 numbers, its rounding and the rest's, 16 bits of mantissa together: with
+// one, out is 1.4 times as far off (2.4e-3 in the 2-norm, of which out's own
+// rounding makes 1.7e-3). y is FP32.
 //
 // A wave's fragment of a block of 128 along k is 16 rows of weights: lane l has
 // 32 values of row l % 16, and of token l % 16's row the same 32, so which
 // values those are is free. The first operand is the tokens, the second the
 // weights: lane l ends with tokens 4 (l / 16) .. + 3 of row l % 16.
+//
+// Both products run in the same form: one workgroup a CU, which takes a run of
+// tasks, each 32 rows of one expert's weights (gated: 16 units, two rows each)
+// for up to 16 MT of its tokens, the blocks along k dealt out to eight waves,
+// whose sums meet in LDS. The tokens' rows stay in registers from task to task
+// (where k fits them), and each register of weights is asked for again, for the
+// next task, as soon as it is widened, so that a CU has 64 KB on their way all
+// the time.
 #include "codec.h"
 #include "launch.h"
 #include "matmul.h"
@@ -30,7 +40,7 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 // What lane l holds of a row's block and of a token's, and what the block's sum is scaled by.
 struct Mx {
-  static constexpr uint32_t kRowBytes = kBlock / 2, kUnroll = 8;
+  static constexpr uint32_t kRowBytes = kBlock / 2;
   typedef uint32_t Scale;  // the row's word of four bytes
   struct Raw {
     u32x4 w;
@@ -45,8 +55,8 @@ struct Mx {
   // value of the token's row that piece p (0 .. 3) of 8 begins at
   static __device__ __forceinline__ uint32_t at(uint32_t q, uint32_t p) { return 32 * q + 8 * p; }
   static __device__ __forceinline__ void widen(const Raw &r, Scale s, uint32_t q, bf16x8 *f) {
-    const uint32_t byte = s >> (8 * q) & 255;
-    const float x = __uint_as_float(byte == 255 ? 0x7FC00000u : byte == 0 ? 0x00400000u : byte << 23);
+    // the conversion takes its scale's exponent field as the byte: 0 is 2^-127, 255 NaN
+    const float x = __uint_as_float(s >> (8 * q) << 23);
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
       const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(r.w[p], x, 0), b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(r.w[p], x, 1);
@@ -62,7 +72,7 @@ struct Mx {
 };
 
 struct F8 {
-  static constexpr uint32_t kRowBytes = kBlock, kUnroll = 4;
+  static constexpr uint32_t kRowBytes = kBlock;
   typedef float Scale;
   struct Raw {
     u32x4 w[2];
@@ -95,25 +105,35 @@ struct F8 {
   }
 };
 
-// The workspace: words[0] the number of experts in use; from words[1] on kMaxGroups entries
-// of (expert, first place in the list, slots); then the list of slots, expert after
-// expert, each expert's in order; then h [slots][pitch] at kHidden.
-constexpr uint32_t kEntry = 3, kList = 4 + kEntry * kMaxGroups, kHidden = (kList + kMlpMaxSlots) * 4;
-static_assert(kHidden % 16 == 0 && kHidden == kMlpHeader, "h is aligned");
+// The workspace: words[0] the number of experts in use; from words[kTable] on for
+// each of those its number, the first place of its slots in the list, and how
+// many they are; at words[kList] the list of slots, expert after expert, each
+// expert's in order; then h, [2][slots][pitch], and y, [slots][pitch].
+constexpr uint32_t kTable = 4, kList = kTable + 3 * kMaxGroups, kHidden = (kList + kMlpMaxSlots) * 4;
+static_assert(kHidden % 16 == 0, "h is aligned");
+
+constexpr uint32_t kWaves = 8, kTaskRows = 32;
 
 struct Args {
   const uint16_t *x;
   const void *ids;
   uint32_t wide;  // 64-bit ids
   const float *weights;
-  const uint8_t *w1, *w2;
-  const void *s1, *s2;
+  const uint8_t *w;  // of this product: [experts][n][k]
+  const void *scales;
   uint32_t *workspace;
   uint16_t *out;
   uint32_t tokens, topk, slots, experts;
-  uint32_t cols, hidden, kblocks1, kblocks2;
-  uint32_t strips;  // of the first kernel's rows
+  uint32_t cols, hidden, h_pitch, y_pitch;
+  uint32_t n, k, kblocks;
+  uint32_t strips;           // tasks that an expert's rows make
+  uint32_t segments, share;  // parts of k that the registers hold at a time; blocks of one that a wave takes
 };
+
+__device__ __forceinline__ uint16_t *h_of(const Args &p, uint32_t plane) {
+  return reinterpret_cast<uint16_t *>(reinterpret_cast<uint8_t *>(p.workspace) + kHidden) + static_cast<uint64_t>(plane) * p.slots * p.h_pitch;
+}
+__device__ __forceinline__ float *y_of(const Args &p) { return reinterpret_cast<float *>(h_of(p, 2)); }
 
 __device__ __forceinline__ uint32_t id_of(const Args &p, uint32_t slot) {
   // an id that is none counts as the expert past the last one
@@ -123,7 +143,6 @@ __device__ __forceinline__ uint32_t id_of(const Args &p, uint32_t slot) {
 
 // Eight values of a row of x from `at` on, zeros from `cols` on.
 __device__ __forceinline__ bf16x8 tokens8(const uint16_t *row, uint32_t at, uint32_t cols) {
-  if (at + 8 <= cols) return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4_any *>(row + at));
   uint32_t e[8];
 #pragma unroll
   for (uint32_t i = 0; i < 8; ++i) e[i] = at + i < cols ? row[at + i] : 0u;
@@ -132,311 +151,385 @@ __device__ __forceinline__ bf16x8 tokens8(const uint16_t *row, uint32_t at, uint
 
 __device__ __forceinline__ float silu(float v) { return v / (1.0f + __expf(-v)); }
 
-// ---------------------------------------------------------------------------
-// h: a workgroup takes one expert and 16 units of h (32 where w1 has no second
-// half), the blocks along k dealt out to its KS waves, whose sums meet in LDS.
-// It finds its expert, the blockIdx-th of those in use, and the expert's
-// slots from the ids by itself; the workgroups of the first strip write the
-// lists down for the second kernel.
-// ---------------------------------------------------------------------------
-template <typename F, uint32_t KS, uint32_t MT, uint32_t U, bool GATED>
-__device__ __forceinline__ void hidden_tile(const Args &p, uint32_t expert, uint32_t unit0, const uint32_t *list, uint32_t count,
-                                            f32x4 (*red)[2][4][kWave]) {
-  const uint32_t lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const uint32_t i16 = lane % 16, q = lane / 16;
-  const uint32_t n = p.hidden * (GATED ? 2 : 1);
-  const uint64_t pitch = static_cast<uint64_t>(p.kblocks1) * F::kRowBytes;
-  const uint8_t *w = p.w1 + static_cast<uint64_t>(expert) * n * pitch;
-  const uint8_t *scales = static_cast<const uint8_t *>(p.s1) + expert * F::scale_bytes(n, p.kblocks1);
-  // rows of w1 past h's units repeat its last one, and their results are not used
-  uint32_t row[2];
-  const uint8_t *from[2];
-#pragma unroll
-  for (uint32_t t = 0; t < 2; ++t) {
-    row[t] = min(unit0 + i16 + (GATED ? 0 : 16 * t), p.hidden - 1) + (GATED ? p.hidden * t : 0);
-    from[t] = w + row[t] * pitch;
-  }
-  const uint16_t *x[MT];
-#pragma unroll
-  for (uint32_t i = 0; i < MT; ++i) x[i] = p.x + static_cast<uint64_t>(list[min(16 * i + i16, count - 1)] / p.topk) * p.cols;
+// The experts in use, in order, and their slots.
+struct Lists {
+  uint32_t expert[kMaxGroups], start[kMaxGroups], count[kMaxGroups];
+  uint32_t passes[kMaxGroups + 1];  // of `tokens` slots each, up to this expert's
+  uint32_t in_use;
+};
 
-  f32x4 acc[MT][2];
+// passes from counts; one wave.
+__device__ __forceinline__ void count_passes(Lists &l, uint32_t tokens) {
+  const uint32_t lane = threadIdx.x % kWave;
+  uint32_t n[4], scan = 0;
 #pragma unroll
-  for (uint32_t i = 0; i < MT; ++i) acc[i][0] = acc[i][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  for (uint32_t kb0 = wave; kb0 < p.kblocks1; kb0 += U * KS) {
-    typename F::Raw raw[U][2];
-    typename F::Scale s[U][2];
-    bf16x8 tok[U][MT][4];
-#pragma unroll
-    for (uint32_t u = 0; u < U; ++u) {
-      const uint32_t kb = min(kb0 + u * KS, p.kblocks1 - 1);  // past the end: loaded again, not used
-#pragma unroll
-      for (uint32_t t = 0; t < 2; ++t) {
-        raw[u][t] = F::load(from[t] + static_cast<uint64_t>(kb) * F::kRowBytes, q);
-        s[u][t] = F::scale(scales, n, kb, row[t]);
-      }
-#pragma unroll
-      for (uint32_t i = 0; i < MT; ++i)
-#pragma unroll
-        for (uint32_t e = 0; e < 4; ++e) tok[u][i][e] = tokens8(x[i], kb * kBlock + F::at(q, e), p.cols);
-    }
-#pragma unroll
-    for (uint32_t u = 0; u < U; ++u) {
-      if (kb0 + u * KS >= p.kblocks1) break;
-#pragma unroll
-      for (uint32_t t = 0; t < 2; ++t) {
-        bf16x8 f[4];
-        F::widen(raw[u][t], s[u][t], q, f);
-#pragma unroll
-        for (uint32_t i = 0; i < MT; ++i) acc[i][t] = F::add(acc[i][t], tok[u][i], f, s[u][t]);
-      }
-    }
+  for (uint32_t i = 0; i < 4; ++i) {
+    n[i] = 4 * lane + i < l.in_use ? (l.count[4 * lane + i] + tokens - 1) / tokens : 0;
+    scan += n[i];
   }
 #pragma unroll
-  for (uint32_t i = 0; i < MT; ++i)
-#pragma unroll
-    for (uint32_t t = 0; t < 2; ++t) red[wave][t][i][lane] = acc[i][t];
-  lds_barrier();
-  uint16_t *h = reinterpret_cast<uint16_t *>(reinterpret_cast<uint8_t *>(p.workspace) + kHidden);
-  for (uint32_t it = wave; it < (GATED ? MT : 2 * MT); it += KS) {
-    const uint32_t i = GATED ? it : it / 2, t = GATED ? 0 : it % 2;
-    f32x4 g = red[0][t][i][lane], u{};
-#pragma unroll
-    for (uint32_t k = 1; k < KS; ++k) g += red[k][t][i][lane];
-    if (GATED) {
-      u = red[0][1][i][lane];
-#pragma unroll
-      for (uint32_t k = 1; k < KS; ++k) u += red[k][1][i][lane];
-    }
-    const uint32_t unit = unit0 + 16 * t + i16;
-#pragma unroll
-    for (uint32_t e = 0; e < 4; ++e) {
-      const uint32_t place = 16 * i + 4 * q + e;
-      // units past the last one, up to the block's end, are zeros
-      const float v = unit < p.hidden ? (GATED ? silu(g[e]) * u[e] : silu(g[e])) : 0.0f;
-      if (place < count && unit < p.kblocks2 * kBlock)
-        h[static_cast<uint64_t>(list[place]) * (p.kblocks2 * kBlock) + unit] = static_cast<uint16_t>(bf16_pair(v, 0.0f));
-    }
+  for (uint32_t d = 1; d < kWave; d *= 2) {
+    const uint32_t up = __shfl_up(scan, d);
+    scan += lane >= d ? up : 0u;
   }
-  lds_barrier();
+  uint32_t before = scan - n[0] - n[1] - n[2] - n[3];
+  if (lane == 0) l.passes[0] = 0;
+#pragma unroll
+  for (uint32_t i = 0; i < 4; ++i) l.passes[4 * lane + i + 1] = before += n[i];
 }
 
-template <typename F, uint32_t KS, bool GATED>
-__global__ __launch_bounds__(KS *kWave) void k_mlp_hidden(Args p) {
-  __shared__ f32x4 red[KS][2][4][kWave];
-  __shared__ uint32_t used[kMaxGroups / 32], list[kMlpMaxSlots], found[2];
-  const uint32_t t = threadIdx.x, lane = t % kWave;
-  const uint32_t strip = blockIdx.x % p.strips, rank = blockIdx.x / p.strips;
-  if (t < kMaxGroups / 32) used[t] = 0;
-  lds_barrier();
-  for (uint32_t s = t; s < p.slots; s += KS * kWave) {
-    const uint32_t id = id_of(p, s);
-    list[s] = id;  // the ids, for now
-    if (id < p.experts) atomicOr(&used[id / 32], 1u << (id % 32));
+// The expert's slots number first .. first + most - 1, in order, to `to`; one wave.
+__device__ __forceinline__ void slots_of(const uint16_t *ids, uint32_t slots, uint32_t expert, uint32_t first, uint32_t most, uint32_t *to) {
+  const uint32_t lane = threadIdx.x % kWave;
+  uint32_t count = 0;
+  for (uint32_t s0 = 0; s0 < slots && count < first + most; s0 += kWave) {
+    const bool mine = s0 + lane < slots && ids[s0 + lane] == expert;
+    const uint64_t all = __ballot(mine);
+    const uint32_t place = count + __popcll(all & ((uint64_t{1} << lane) - 1));
+    if (mine && place >= first && place < first + most) to[place - first] = s0 + lane;
+    count += __popcll(all);
   }
-  lds_barrier();
-  uint32_t expert = p.experts, in_use = 0;
+}
+
+// U blocks along k a wave and segment at most, 16 MT tokens a pass. OUT: y from h, else h from x.
+// WHOLE: k is a multiple of 8.
+template <typename F, uint32_t U, uint32_t MT, bool OUT, bool GATED, bool WHOLE>
+__global__ __launch_bounds__(kWaves *kWave) void k_mlp(Args p) {
+  constexpr uint32_t kPlanes = OUT ? 2 : 1, kTokens = 16 * MT;
+  constexpr uint32_t kGroups = MT * (GATED ? 1 : 2);  // results of 16 x 16 of a task
+  __shared__ f32x4 red[2][kWaves][2][MT][kWave];
+  __shared__ Lists lists;
+  __shared__ uint16_t ids[OUT ? 1 : kMlpMaxSlots];
+  __shared__ uint32_t of_pass[kWaves][kTokens];  // each wave's own copy
+  const uint32_t lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const uint32_t i16 = lane % 16, q = lane / 16;
+
+  if (OUT) {
+    for (uint32_t i = threadIdx.x; i < kMaxGroups; i += kWaves * kWave) {
+      lists.expert[i] = p.workspace[kTable + i];
+      lists.start[i] = p.workspace[kTable + kMaxGroups + i];
+      lists.count[i] = p.workspace[kTable + 2 * kMaxGroups + i];
+    }
+    if (threadIdx.x == 0) lists.in_use = p.workspace[0];
+    __syncthreads();
+  } else {
+    // count every expert's slots, then number the experts that have some
+    uint32_t *counts = reinterpret_cast<uint32_t *>(&red[0][0][0][0][0]);
+    if (threadIdx.x < kMaxGroups) counts[threadIdx.x] = 0;
+    lds_barrier();
+    for (uint32_t s = threadIdx.x; s < p.slots; s += kWaves * kWave) {
+      const uint32_t id = id_of(p, s);
+      ids[s] = static_cast<uint16_t>(id);
+      if (id < p.experts) atomicAdd(&counts[id], 1u);
+    }
+    lds_barrier();
+    if (wave == 0) {
+      uint32_t n[4], scan = 0;  // experts in use << 16 | slots
 #pragma unroll
-  for (uint32_t i = 0; i < kMaxGroups / 32; ++i) {
-    uint32_t w = used[i];
-    const uint32_t n = __popc(w);
-    if (rank >= in_use && rank < in_use + n) {
-      for (uint32_t skip = rank - in_use; skip > 0; --skip) w &= w - 1;
-      expert = 32 * i + static_cast<uint32_t>(__builtin_ctz(w));
+      for (uint32_t i = 0; i < 4; ++i) {
+        n[i] = counts[4 * lane + i];
+        scan += n[i] | (n[i] > 0 ? 1u << 16 : 0u);
+      }
+      const uint32_t own = scan;
+#pragma unroll
+      for (uint32_t d = 1; d < kWave; d *= 2) {
+        const uint32_t up = __shfl_up(scan, d);
+        scan += lane >= d ? up : 0u;
+      }
+      uint32_t rank = (scan - own) >> 16, start = (scan - own) & 0xFFFF;
+#pragma unroll
+      for (uint32_t i = 0; i < 4; ++i) {
+        if (n[i] == 0) continue;
+        lists.expert[rank] = 4 * lane + i;
+        lists.start[rank] = start;
+        lists.count[rank] = n[i];
+        ++rank, start += n[i];
+      }
+      if (lane == kWave - 1) lists.in_use = scan >> 16;
     }
-    in_use += n;
-  }
-  expert = __builtin_amdgcn_readfirstlane(expert);
-  if (strip == 0 && rank == 0 && t == 0) p.workspace[0] = in_use;
-  if (expert == p.experts) return;
-  if (t < kWave) {  // one wave puts the expert's slots in order; what it writes is behind what it reads
-    uint32_t count = 0, before = 0;
-    for (uint32_t s0 = 0; s0 < p.slots; s0 += kWave) {
-      const uint32_t id = s0 + lane < p.slots ? list[s0 + lane] : p.experts;
-      const uint64_t mine = __ballot(id == expert);
-      before += __popcll(__ballot(id < expert));
-      if (id == expert) list[count + __popcll(mine & ((uint64_t{1} << lane) - 1))] = s0 + lane;
-      count += __popcll(mine);
+    lds_barrier();
+    // the second kernel's copy: a workgroup writes down the lists of every so-manyth expert
+    const uint32_t in_use = __builtin_amdgcn_readfirstlane(lists.in_use);
+    if (blockIdx.x == 0 && threadIdx.x == 0) p.workspace[0] = in_use;
+    if (wave == kWaves - 1) {
+      for (uint32_t r = blockIdx.x; r < in_use; r += gridDim.x) {
+        const uint32_t expert = __builtin_amdgcn_readfirstlane(lists.expert[r]), start = __builtin_amdgcn_readfirstlane(lists.start[r]);
+        const uint32_t count = __builtin_amdgcn_readfirstlane(lists.count[r]);
+        if (lane == 0) {
+          p.workspace[kTable + r] = expert;
+          p.workspace[kTable + kMaxGroups + r] = start;
+          p.workspace[kTable + 2 * kMaxGroups + r] = count;
+        }
+        slots_of(ids, p.slots, expert, 0, count, p.workspace + kList + start);
+      }
     }
-    if (lane == 0) found[0] = count, found[1] = before;
   }
+  if (wave == 0) count_passes(lists, kTokens);
   lds_barrier();
-  const uint32_t count = __builtin_amdgcn_readfirstlane(found[0]);
-  if (strip == 0) {
-    const uint32_t before = __builtin_amdgcn_readfirstlane(found[1]);
-    if (t < kEntry) p.workspace[1 + kEntry * rank + t] = t == 0 ? expert : t == 1 ? before : count;
-    for (uint32_t i = t; i < count; i += KS * kWave) p.workspace[kList + before + i] = list[i];
-  }
-  const uint32_t unit0 = strip * (GATED ? 16 : 32);
-  for (uint32_t at = 0; at < count;) {
-    const uint32_t left = count - at;
-    if (left <= 16) {
-      hidden_tile<F, KS, 1, 4, GATED>(p, expert, unit0, list + at, left, red);
-      at += 16;
-    } else if (left <= 32) {
-      hidden_tile<F, KS, 2, 2, GATED>(p, expert, unit0, list + at, left, red);
-      at += 32;
+
+  // this workgroup's tasks: pass after pass, strip after strip
+  const uint64_t tasks = static_cast<uint64_t>(__builtin_amdgcn_readfirstlane(lists.passes[kMaxGroups])) * p.strips;
+  const uint64_t first_task = tasks * blockIdx.x / gridDim.x, end_task = tasks * (blockIdx.x + 1) / gridDim.x;
+  if (first_task >= end_task) return;
+
+  struct Task {
+    uint32_t pass, strip, segment;
+    uint32_t rank, expert;
+  };
+  auto settle = [&](Task &t) {  // the pass's expert
+    while (t.pass >= __builtin_amdgcn_readfirstlane(lists.passes[t.rank + 1])) ++t.rank;
+    t.expert = __builtin_amdgcn_readfirstlane(lists.expert[t.rank]);
+  };
+  const uint64_t pitch = static_cast<uint64_t>(p.kblocks) * F::kRowBytes, scale_bytes = F::scale_bytes(p.n, p.kblocks);
+  typename F::Raw raw[U][2];
+  typename F::Scale scale[U][2];
+  struct From {
+    const uint8_t *row[2];
+    const uint8_t *scales;
+    uint32_t at[2];  // rows of the matrix; those past the end repeat the last one, and their results are not used
+  };
+  auto block_of = [&](uint32_t segment, uint32_t u) { return (segment * kWaves + wave) * p.share + u; };
+  auto from_of = [&](const Task &t) {
+    From f;
+    const uint8_t *matrix = p.w + static_cast<uint64_t>(t.expert) * p.n * pitch;
+    f.scales = static_cast<const uint8_t *>(p.scales) + t.expert * scale_bytes;
+#pragma unroll
+    for (uint32_t i = 0; i < 2; ++i) {
+      if (GATED) f.at[i] = min(t.strip * 16 + i16, p.hidden - 1) + i * p.hidden;
+      else f.at[i] = min(t.strip * 32 + 16 * i + i16, p.n - 1);
+      f.row[i] = matrix + f.at[i] * pitch;
+    }
+    return f;
+  };
+  auto load = [&](const From &f, const Task &t, uint32_t u) {
+    const uint32_t kb = min(block_of(t.segment, min(u, p.share - 1)), p.kblocks - 1);  // past the end: loaded again, not used
+#pragma unroll
+    for (uint32_t i = 0; i < 2; ++i) {
+      raw[u][i] = F::load(f.row[i] + static_cast<uint64_t>(kb) * F::kRowBytes, q);
+      scale[u][i] = F::scale(f.scales, p.n, kb, f.at[i]);
+    }
+  };
+  bf16x8 tok[U][MT][kPlanes][4];
+  uint32_t count = 0;  // the pass's tokens
+  auto load_tokens = [&](const Task &t) {
+    const uint32_t first = (t.pass - __builtin_amdgcn_readfirstlane(lists.passes[t.rank])) * kTokens;
+    count = min(kTokens, __builtin_amdgcn_readfirstlane(lists.count[t.rank]) - first);
+    if (OUT) {
+      if (lane < count) of_pass[wave][lane] = p.workspace[kList + lists.start[t.rank] + first + lane];
     } else {
-      hidden_tile<F, KS, 4, 1, GATED>(p, expert, unit0, list + at, min(left, 64u), red);
-      at += 64;
+      slots_of(ids, p.slots, t.expert, first, kTokens, of_pass[wave]);
     }
-  }
-}
-
-// ---------------------------------------------------------------------------
-// out: a workgroup takes 16 columns. Its waves go through the experts in use,
-// each expert by one wave or (few experts) its blocks along k by `parts` of
-// them, and leave each slot's product with the expert's 16 rows in LDS, where
-// they are added up in the order of the choices: no atomics, and nothing but
-// out is written to memory. The next chunk of weights is on its way while one
-// is multiplied.
-// ---------------------------------------------------------------------------
-constexpr uint32_t kOutWaves = 8, kOutCols = 16;
-constexpr uint32_t kSums = 1024;  // slots times parts that LDS has room for
-
-template <typename F>
-__global__ __launch_bounds__(kOutWaves *kWave) void k_mlp_out(Args p) {
-  constexpr uint32_t U = F::kUnroll;
-  __shared__ float sums[kSums][kOutCols];
-  __shared__ uint32_t table[kList + kMlpMaxSlots];
-  const uint32_t lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const uint32_t i16 = lane % 16, q = lane / 16;
-  const uint32_t c0 = blockIdx.x * kOutCols;
-  for (uint32_t i = threadIdx.x; i < kList + p.slots; i += kOutWaves * kWave) table[i] = p.workspace[i];
-  lds_barrier();
-  const uint32_t in_use = __builtin_amdgcn_readfirstlane(table[0]);
-  const uint32_t *const list = table + kList;
-
-  // parts: as many as there are waves for, chunks of U blocks to deal out, and room in LDS
-  const uint32_t chunks_all = (p.kblocks2 + U - 1) / U;
-  uint32_t parts = in_use == 0 ? 1 : max(1u, min(min(kOutWaves / in_use, chunks_all), kSums / p.slots));
-  const uint32_t per_part = (chunks_all + parts - 1) / parts;
-  const uint32_t items = in_use * parts;
-  const uint64_t pitch = static_cast<uint64_t>(p.kblocks2) * F::kRowBytes;
-  const uint32_t row = min(c0 + i16, p.cols - 1);
-  const uint16_t *h = reinterpret_cast<const uint16_t *>(reinterpret_cast<const uint8_t *>(p.workspace) + kHidden);
-  const uint32_t h_pitch = p.kblocks2 * kBlock;
-
-  struct Chunk {
-    typename F::Raw raw[U];
-    typename F::Scale s[U];
-  };
-  struct Where {
-    uint32_t item, pass, chunk;  // pass: of 32 slots of the expert
-  };
-  auto expert_of = [&](uint32_t item) { return __builtin_amdgcn_readfirstlane(table[1 + kEntry * (item / parts)]); };
-  auto count_of = [&](uint32_t item) { return __builtin_amdgcn_readfirstlane(table[1 + kEntry * (item / parts) + 2]); };
-  auto chunks_of = [&](uint32_t item) {  // this part's
-    const uint32_t first = item % parts * per_part;
-    return first >= chunks_all ? 0 : min(per_part, chunks_all - first);
-  };
-  auto next = [&](Where at) {
-    if (++at.chunk < chunks_of(at.item)) return at;
-    at.chunk = 0;
-    if (32 * ++at.pass < count_of(at.item)) return at;
-    at.pass = 0;
-    at.item += kOutWaves;
-    return at;
-  };
-  auto load = [&](const Where &at, Chunk &c) {
-    const uint32_t expert = expert_of(at.item);
-    const uint8_t *from = p.w2 + (static_cast<uint64_t>(expert) * p.cols + row) * pitch;
-    const uint8_t *scales = static_cast<const uint8_t *>(p.s2) + expert * F::scale_bytes(p.cols, p.kblocks2);
+    __builtin_amdgcn_wave_barrier();
+    const uint16_t *row[MT];
 #pragma unroll
-    for (uint32_t u = 0; u < U; ++u) {
-      const uint32_t kb = min((at.item % parts * per_part + at.chunk) * U + u, p.kblocks2 - 1);
-      c.raw[u] = F::load(from + static_cast<uint64_t>(kb) * F::kRowBytes, q);
-      c.s[u] = F::scale(scales, p.cols, kb, row);
+    for (uint32_t m = 0; m < MT; ++m) {
+      const uint32_t slot = of_pass[wave][min(16 * m + i16, count - 1)];
+      row[m] = OUT ? h_of(p, 0) + static_cast<uint64_t>(slot) * p.h_pitch : p.x + static_cast<uint64_t>(slot / p.topk) * p.cols;
     }
-  };
-
-  Where at{wave, 0, 0};
-  Chunk now, ahead;
-  f32x4 acc[2];
-  if (at.item < items) load(at, now);
-  while (at.item < items) {
-    const Where then = next(at);
-    if (then.item < items) load(then, ahead);
-    const uint32_t first = __builtin_amdgcn_readfirstlane(table[1 + kEntry * (at.item / parts) + 1]) + 32 * at.pass;
-    const uint32_t count = min(32u, count_of(at.item) - 32 * at.pass);
-    if (at.chunk == 0) acc[0] = acc[1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    const uint32_t kb0 = (at.item % parts * per_part + at.chunk) * U;
-    const uint16_t *tok[2];
-#pragma unroll
-    for (uint32_t i = 0; i < 2; ++i) tok[i] = h + static_cast<uint64_t>(list[first + min(16 * i + i16, count - 1)]) * h_pitch;
-    if (chunks_of(at.item) > 0) {
+    const uint64_t plane = OUT ? static_cast<uint64_t>(p.slots) * p.h_pitch : 0;
+    if constexpr (WHOLE) {  // pieces of eight are whole, or past the end
 #pragma unroll
       for (uint32_t u = 0; u < U; ++u) {
-        if (kb0 + u >= p.kblocks2) break;
-        bf16x8 f[4];
-        F::widen(now.raw[u], now.s[u], q, f);
+        const uint32_t kb = min(block_of(t.segment, min(u, p.share - 1)), p.kblocks - 1);
 #pragma unroll
-        for (uint32_t i = 0; i < 2; ++i) {
-          if (16 * i >= count) break;
-          bf16x8 t[4];
+        for (uint32_t m = 0; m < MT; ++m)
 #pragma unroll
-          for (uint32_t e = 0; e < 4; ++e) t[e] = *reinterpret_cast<const bf16x8 *>(tok[i] + (kb0 + u) * kBlock + F::at(q, e));
-          acc[i] = F::add(acc[i], t, f, now.s[u]);
-        }
+          for (uint32_t l = 0; l < kPlanes; ++l)
+#pragma unroll
+            for (uint32_t e = 0; e < 4; ++e) {
+              const uint32_t at = kb * kBlock + F::at(q, e);
+              const u32x4 w = *reinterpret_cast<const u32x4 *>(row[m] + l * plane + (OUT ? at : min(at, p.cols - 8)));
+              tok[u][m][l][e] = __builtin_bit_cast(bf16x8, OUT || at < p.cols ? w : u32x4{0, 0, 0, 0});
+            }
+      }
+    } else {
+#pragma unroll
+      for (uint32_t u = 0; u < U; ++u) {
+        const uint32_t kb = min(block_of(t.segment, min(u, p.share - 1)), p.kblocks - 1);
+#pragma unroll
+        for (uint32_t m = 0; m < MT; ++m)
+#pragma unroll
+          for (uint32_t e = 0; e < 4; ++e) {
+            tok[u][m][0][e] = tokens8(row[m], kb * kBlock + F::at(q, e), p.cols);
+            __builtin_amdgcn_sched_barrier(0);  // (else all of them are on their way at once, in eight registers each)
+          }
       }
     }
-    if (then.chunk == 0) {  // the pass is done
+  };
+
+  Task now{static_cast<uint32_t>(first_task / p.strips), static_cast<uint32_t>(first_task % p.strips), 0, 0, 0};
+  settle(now);
+  {
+    const From f = from_of(now);
+#pragma unroll
+    for (uint32_t u = 0; u < U; ++u) load(f, now, u);
+  }
+  load_tokens(now);
+  uint32_t buffer = 0;
+  f32x4 acc[MT][2];
+  for (uint64_t task = first_task; task < end_task;) {
+    if (now.segment == 0) {
+#pragma unroll
+      for (uint32_t m = 0; m < MT; ++m) acc[m][0] = acc[m][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    Task next = now;
+    const bool last_segment = ++next.segment == p.segments;
+    if (last_segment) {
+      next.segment = 0;
+      if (++next.strip == p.strips) next.strip = 0, ++next.pass;
+    }
+    const bool more = !last_segment || task + 1 < end_task;
+    if (more) settle(next);
+    From f = from_of(more ? next : now);
+    if (!more) f.row[0] = f.row[1] = p.w;  // nothing is left to load: a line that all of the wave reads
+#pragma unroll
+    for (uint32_t u = 0; u < U; ++u) {
+      bf16x8 w[2][4];
+      typename F::Scale s[2];
+#pragma unroll
+      for (uint32_t i = 0; i < 2; ++i) {
+        F::widen(raw[u][i], scale[u][i], q, w[i]);
+        s[i] = scale[u][i];
+      }
+      load(f, next, u);
+      if (u >= p.share || block_of(now.segment, u) >= p.kblocks) continue;
 #pragma unroll
       for (uint32_t i = 0; i < 2; ++i)
 #pragma unroll
-        for (uint32_t e = 0; e < 4; ++e) {
-          const uint32_t place = 16 * i + 4 * q + e;
-          if (place < count) sums[at.item % parts * p.slots + list[first + place]][i16] = acc[i][e];
+        for (uint32_t m = 0; m < MT; ++m)
+#pragma unroll
+          for (uint32_t l = 0; l < kPlanes; ++l) acc[m][i] = F::add(acc[m][i], tok[u][m][l], w[i], s[i]);
+    }
+    if (last_segment) {
+#pragma unroll
+      for (uint32_t m = 0; m < MT; ++m)
+#pragma unroll
+        for (uint32_t i = 0; i < 2; ++i) red[buffer][wave][i][m][lane] = acc[m][i];
+      lds_barrier();  // (the next task's sums go to the other buffer, so one is enough)
+      for (uint32_t it = wave; it < 4 * kGroups; it += kWaves) {
+        const uint32_t group = it / 4, e = it % 4, m = GATED ? group : group / 2, i = GATED ? 0 : group % 2;
+        auto sum = [&](uint32_t i) {
+          float v = red[buffer][0][i][m][lane][e];
+#pragma unroll
+          for (uint32_t k = 1; k < kWaves; ++k) v += red[buffer][k][i][m][lane][e];
+          return v;
+        };
+        const float v = sum(i);
+        const uint32_t place = 16 * m + 4 * q + e;
+        if (OUT) {
+          const uint32_t c = now.strip * 32 + 16 * i + i16;  // (y's rows go on to the end of the strip)
+          if (place < count) y_of(p)[static_cast<uint64_t>(of_pass[wave][place]) * p.y_pitch + c] = v;
+        } else {
+          const uint32_t unit = now.strip * (GATED ? 16 : 32) + 16 * i + i16;
+          // units past the last one, up to the block's end, are zeros
+          const float h = unit < p.hidden ? (GATED ? silu(v) * sum(1) : silu(v)) : 0.0f;
+          if (place < count && unit < p.h_pitch) {
+            const uint64_t at = static_cast<uint64_t>(of_pass[wave][place]) * p.h_pitch + unit;
+            const uint32_t hi = bf16_pair(h, 0.0f) & 0xFFFF;
+            // (where the rounding is no number, or infinite, so that the sum shall be, the rest is nothing)
+            const float rest = h - __uint_as_float(hi << 16);
+            h_of(p, 0)[at] = static_cast<uint16_t>(hi);
+            h_of(p, 1)[at] = static_cast<uint16_t>(bf16_pair(fabsf(rest) <= fabsf(h) ? rest : 0.0f, 0.0f));
+          }
         }
+      }
+      buffer ^= 1;
+      ++task;
     }
-    now = ahead;
-    at = then;
-  }
-  lds_barrier();
-  for (uint32_t i = threadIdx.x; i < p.tokens * kOutCols; i += kOutWaves * kWave) {
-    const uint32_t t = i / kOutCols, c = i % kOutCols;
-    float v = 0.0f;
-    for (uint32_t j = 0; j < p.topk; ++j) {
-      const uint32_t slot = t * p.topk + j;
-      if (id_of(p, slot) == p.experts) continue;
-      float y = 0.0f;
-      for (uint32_t k = 0; k < parts; ++k) y += sums[k * p.slots + slot][c];
-      v += p.weights[slot] * y;
-    }
-    if (c0 + c < p.cols) p.out[static_cast<uint64_t>(t) * p.cols + c0 + c] = static_cast<uint16_t>(bf16_pair(v, 0.0f));
+    if (more && (p.segments > 1 || next.pass != now.pass)) load_tokens(next);
+    now = next;
   }
 }
 
-template <typename F, uint32_t KS>
-hipError_t launch_hidden(const Args &a, bool gated, hipStream_t s) {
-  const uint64_t blocks = static_cast<uint64_t>(a.strips) * min(a.experts, a.slots);
-  if (blocks * KS * kWave >= kMaxThreads1D) return hipErrorInvalidConfiguration;
-  if (gated) hipLaunchKernelGGL((k_mlp_hidden<F, KS, true>), dim3(static_cast<uint32_t>(blocks)), dim3(KS * kWave), 0, s, a);
-  else hipLaunchKernelGGL((k_mlp_hidden<F, KS, false>), dim3(static_cast<uint32_t>(blocks)), dim3(KS * kWave), 0, s, a);
+// ---------------------------------------------------------------------------
+// out: four columns of a token to a thread, its slots in the order of the choices.
+// ---------------------------------------------------------------------------
+constexpr uint32_t kCombineThreads = 256;
+__global__ __launch_bounds__(kCombineThreads) void k_mlp_combine(Args p, uint32_t per_row) {
+  const uint32_t t = blockIdx.x / per_row, c = (blockIdx.x % per_row * kCombineThreads + threadIdx.x) * 4;
+  if (c >= p.cols) return;
+  const float *y = y_of(p);
+  f32x4 v{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+  for (uint32_t j = 0; j < p.topk; ++j) {
+    const uint32_t slot = t * p.topk + j;
+    if (id_of(p, slot) == p.experts) continue;
+    v += p.weights[slot] * *reinterpret_cast<const f32x4 *>(y + static_cast<uint64_t>(slot) * p.y_pitch + c);
+  }
+  store4<false>(p.out, static_cast<uint64_t>(t) * p.cols, c, p.cols, v);
+}
+
+uint32_t h_pitch(uint64_t hidden) { return static_cast<uint32_t>((hidden + kBlock - 1) / kBlock * kBlock); }
+uint32_t y_pitch(uint64_t cols) { return static_cast<uint32_t>((cols + kTaskRows - 1) / kTaskRows * kTaskRows); }
+
+constexpr uint32_t kWorkgroups = 256;  // one a CU
+
+template <typename F, uint32_t U, uint32_t MT, bool OUT, bool WHOLE = true>
+hipError_t launch_product(Args a, bool gated, hipStream_t s) {
+  a.kblocks = (a.k + kBlock - 1) / kBlock;
+  a.segments = (a.kblocks + kWaves * U - 1) / (kWaves * U);
+  a.share = (a.kblocks + kWaves * a.segments - 1) / (kWaves * a.segments);
+  // rows of h up to the end of its last block, so that what the second kernel reads is written
+  a.strips = OUT ? a.y_pitch / 32 : a.h_pitch / (gated ? 16 : 32);
+  const uint64_t passes = min(a.experts, a.slots) + a.slots / (16 * MT);
+  const dim3 grid(static_cast<uint32_t>(min(static_cast<uint64_t>(kWorkgroups), passes * a.strips)));
+  if (gated) hipLaunchKernelGGL((k_mlp<F, U, MT, OUT, !OUT, WHOLE>), grid, dim3(kWaves * kWave), 0, s, a);
+  else hipLaunchKernelGGL((k_mlp<F, U, MT, OUT, false, WHOLE>), grid, dim3(kWaves * kWave), 0, s, a);
   return hipGetLastError();
 }
 
-template <typename F>
-hipError_t launch(const Args &a, bool gated, hipStream_t s) {
-  const hipError_t e = a.kblocks1 >= 8 ? launch_hidden<F, 8>(a, gated, s) : launch_hidden<F, 2>(a, gated, s);
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((k_mlp_out<F>), dim3((a.cols + kOutCols - 1) / kOutCols), dim3(kOutWaves * kWave), 0, s, a);
-  return hipGetLastError();
+// What the registers hold of a wave's share of k: blocks U times tokens 16 MT (times two numbers for h).
+hipError_t launch_hidden(const Args &a, bool fp8, bool gated, hipStream_t s) {
+  const uint32_t share = (a.k + kBlock * kWaves - 1) / (kBlock * kWaves);
+  const bool few = a.slots <= 16;
+  if (a.k % 8 != 0) return fp8 ? launch_product<F8, 2, 1, false, false>(a, gated, s) : launch_product<Mx, 2, 1, false, false>(a, gated, s);
+  if (fp8) return share <= 2 ? launch_product<F8, 2, 1, false>(a, gated, s) : launch_product<F8, 5, 1, false>(a, gated, s);
+  if (few) return share <= 2 ? launch_product<Mx, 2, 1, false>(a, gated, s) : launch_product<Mx, 4, 1, false>(a, gated, s);
+  return share <= 2 ? launch_product<Mx, 2, 2, false>(a, gated, s) : launch_product<Mx, 4, 2, false>(a, gated, s);
+}
+hipError_t launch_out(const Args &a, bool fp8, hipStream_t s) {
+  const uint32_t share = (a.k + kBlock * kWaves - 1) / (kBlock * kWaves);
+  if (fp8) return launch_product<F8, 2, 1, true>(a, false, s);
+  if (share > 2) return launch_product<Mx, 4, 1, true>(a, false, s);
+  return a.slots <= 16 ? launch_product<Mx, 2, 1, true>(a, false, s) : launch_product<Mx, 2, 2, true>(a, false, s);
 }
 
 }  // namespace
 
-uint64_t expert_mlp_workspace_bytes(uint64_t slots, uint64_t hidden) {
-  return kHidden + slots * ((hidden + kBlock - 1) / kBlock * kBlock) * 2;
+uint64_t expert_mlp_workspace_bytes(uint64_t slots, uint64_t cols, uint64_t hidden) {
+  return kHidden + slots * (4 * static_cast<uint64_t>(h_pitch(hidden)) + 4 * static_cast<uint64_t>(y_pitch(cols)));
 }
 
 hipError_t launch_expert_mlp(const ExpertMlp &p, hipStream_t s) {
-  Args a{static_cast<const uint16_t *>(p.x), p.ids, p.wide, p.weights, p.w1, p.w2, p.s1, p.s2, p.workspace, static_cast<uint16_t *>(p.out),
-         p.tokens, p.topk, p.tokens * p.topk, p.experts, p.cols, p.hidden, (p.cols + kBlock - 1) / kBlock, (p.hidden + kBlock - 1) / kBlock, 0};
-  // units up to the end of the last block, so that what the second kernel reads of h is written
-  const uint32_t units = a.kblocks2 * kBlock, each = p.gated ? 16 : 32;
-  a.strips = (units + each - 1) / each;
-  return p.fp8 ? launch<F8>(a, p.gated, s) : launch<Mx>(a, p.gated, s);
+  Args a{};
+  a.x = static_cast<const uint16_t *>(p.x);
+  a.ids = p.ids;
+  a.wide = p.wide;
+  a.weights = p.weights;
+  a.workspace = p.workspace;
+  a.out = static_cast<uint16_t *>(p.out);
+  a.tokens = p.tokens;
+  a.topk = p.topk;
+  a.slots = p.tokens * p.topk;
+  a.experts = p.experts;
+  a.cols = p.cols;
+  a.hidden = p.hidden;
+  a.h_pitch = h_pitch(p.hidden);
+  a.y_pitch = y_pitch(p.cols);
+  a.w = p.w1;
+  a.scales = p.s1;
+  a.n = p.hidden * (p.gated ? 2 : 1);
+  a.k = p.cols;
+  hipError_t e = launch_hidden(a, p.fp8, p.gated, s);
+  if (e != hipSuccess) return e;
+  a.w = p.w2;
+  a.scales = p.s2;
+  a.n = p.cols;
+  a.k = p.hidden;
+  if ((e = launch_out(a, p.fp8, s)) != hipSuccess) return e;
+  const uint32_t per_row = (p.cols + 4 * kCombineThreads - 1) / (4 * kCombineThreads);
+  hipLaunchKernelGGL(k_mlp_combine, dim3(p.tokens * per_row), dim3(kCombineThreads), 0, s, a, per_row);
+  return hipGetLastError();
 }
 
 }  // namespace nvfp4

@@ -289,7 +289,6 @@ hipError_t launch_mxfp4_matmul(const Mxfp4Matmul &p, hipStream_t s);
 
 // The expert layer for a few tokens; nothing is empty but the dropped slots.
 constexpr uint32_t kMlpMaxSlots = 1024;
-constexpr uint32_t kMlpHeader = (1 + 3 * kMaxGroups + 3 + kMlpMaxSlots) * 4;
 struct ExpertMlp {
   const void *x;  // BF16 [tokens][cols]
   const void *ids;
@@ -302,7 +301,7 @@ struct ExpertMlp {
   void *out;  // BF16 [tokens][cols]
   uint32_t tokens, topk, experts, cols, hidden;
 };
-uint64_t expert_mlp_workspace_bytes(uint64_t slots, uint64_t hidden);
+uint64_t expert_mlp_workspace_bytes(uint64_t slots, uint64_t cols, uint64_t hidden);
 hipError_t launch_expert_mlp(const ExpertMlp &p, hipStream_t s);
 
 hipError_t launch_debug_e2m1(const float *v, const uint32_t *r, uint8_t *out, uint64_t n, bool sr, bool pairwise,
