@@ -20,8 +20,8 @@
 // weights: lane l ends with tokens 4 (l / 16) .. + 3 of row l % 16.
 //
 // Both products run in the same form: one workgroup a CU, which takes a run of
-// tasks, each 32 rows of one expert's weights (gated: 16 units, two rows each)
-// for up to 16 MT of its tokens, the blocks along k dealt out to eight waves,
+// tasks, each 16 NT rows of one expert's weights (gated: two rows for each of 8 NT
+// units) for up to 16 MT of its tokens, the blocks along k dealt out to eight waves,
 // whose sums meet in LDS. The tokens' rows stay in registers from task to task
 // (where k fits them), and each register of weights is asked for again, for the
 // next task, as soon as it is widened, so that a CU has 64 KB on their way all
@@ -112,7 +112,7 @@ struct F8 {
 constexpr uint32_t kTable = 4, kList = kTable + 3 * kMaxGroups, kHidden = (kList + kMlpMaxSlots) * 4;
 static_assert(kHidden % 16 == 0, "h is aligned");
 
-constexpr uint32_t kWaves = 8, kTaskRows = 32;
+constexpr uint32_t kWaves = 8, kMostRows = 64;  // of a task
 
 struct Args {
   const uint16_t *x;
@@ -191,13 +191,14 @@ __device__ __forceinline__ void slots_of(const uint16_t *ids, uint32_t slots, ui
   }
 }
 
-// U blocks along k a wave and segment at most, 16 MT tokens a pass. OUT: y from h, else h from x.
+// U blocks along k a wave and segment at most, 16 MT tokens a pass, 16 NT rows a task. OUT: y from h, else h from x.
 // WHOLE: k is a multiple of 8.
-template <typename F, uint32_t U, uint32_t MT, bool OUT, bool GATED, bool WHOLE>
+template <typename F, uint32_t U, uint32_t MT, uint32_t NT, bool OUT, bool GATED, bool WHOLE>
 __global__ __launch_bounds__(kWaves *kWave) void k_mlp(Args p) {
   constexpr uint32_t kPlanes = OUT ? 2 : 1, kTokens = 16 * MT;
-  constexpr uint32_t kGroups = MT * (GATED ? 1 : 2);  // results of 16 x 16 of a task
-  __shared__ f32x4 red[2][kWaves][2][MT][kWave];
+  constexpr uint32_t kWide = GATED ? NT / 2 : NT, kGroups = MT * kWide;  // results of 16 x 16 of a task
+  static_assert(16 * NT <= kMostRows, "what the pitches allow for");
+  __shared__ f32x4 red[2][kWaves][NT][MT][kWave];
   __shared__ Lists lists;
   __shared__ uint16_t ids[OUT ? 1 : kMlpMaxSlots];
   __shared__ uint32_t of_pass[kWaves][kTokens];  // each wave's own copy
@@ -281,12 +282,12 @@ __global__ __launch_bounds__(kWaves *kWave) void k_mlp(Args p) {
     t.expert = __builtin_amdgcn_readfirstlane(lists.expert[t.rank]);
   };
   const uint64_t pitch = static_cast<uint64_t>(p.kblocks) * F::kRowBytes, scale_bytes = F::scale_bytes(p.n, p.kblocks);
-  typename F::Raw raw[U][2];
-  typename F::Scale scale[U][2];
+  typename F::Raw raw[U][NT];
+  typename F::Scale scale[U][NT];
   struct From {
-    const uint8_t *row[2];
+    const uint8_t *row[NT];
     const uint8_t *scales;
-    uint32_t at[2];  // rows of the matrix; those past the end repeat the last one, and their results are not used
+    uint32_t at[NT];  // rows of the matrix; those past the end repeat the last one, and their results are not used
   };
   auto block_of = [&](uint32_t segment, uint32_t u) { return (segment * kWaves + wave) * p.share + u; };
   auto from_of = [&](const Task &t) {
@@ -294,20 +295,16 @@ __global__ __launch_bounds__(kWaves *kWave) void k_mlp(Args p) {
     const uint8_t *matrix = p.w + static_cast<uint64_t>(t.expert) * p.n * pitch;
     f.scales = static_cast<const uint8_t *>(p.scales) + t.expert * scale_bytes;
 #pragma unroll
-    for (uint32_t i = 0; i < 2; ++i) {
-      if (GATED) f.at[i] = min(t.strip * 16 + i16, p.hidden - 1) + i * p.hidden;
-      else f.at[i] = min(t.strip * 32 + 16 * i + i16, p.n - 1);
+    for (uint32_t i = 0; i < NT; ++i) {
+      f.at[i] = min((t.strip * kWide + i % kWide) * 16 + i16, (OUT ? p.n : p.hidden) - 1) + i / kWide * p.hidden;
       f.row[i] = matrix + f.at[i] * pitch;
     }
     return f;
   };
-  auto load = [&](const From &f, const Task &t, uint32_t u) {
+  auto load = [&](const From &f, const Task &t, uint32_t u, uint32_t i) {
     const uint32_t kb = min(block_of(t.segment, min(u, p.share - 1)), p.kblocks - 1);  // past the end: loaded again, not used
-#pragma unroll
-    for (uint32_t i = 0; i < 2; ++i) {
-      raw[u][i] = F::load(f.row[i] + static_cast<uint64_t>(kb) * F::kRowBytes, q);
-      scale[u][i] = F::scale(f.scales, p.n, kb, f.at[i]);
-    }
+    raw[u][i] = F::load(f.row[i] + static_cast<uint64_t>(kb) * F::kRowBytes, q);
+    scale[u][i] = F::scale(f.scales, p.n, kb, f.at[i]);
   };
   bf16x8 tok[U][MT][kPlanes][4];
   uint32_t count = 0;  // the pass's tokens
@@ -362,15 +359,19 @@ __global__ __launch_bounds__(kWaves *kWave) void k_mlp(Args p) {
   {
     const From f = from_of(now);
 #pragma unroll
-    for (uint32_t u = 0; u < U; ++u) load(f, now, u);
+    for (uint32_t u = 0; u < U; ++u)
+#pragma unroll
+      for (uint32_t i = 0; i < NT; ++i) load(f, now, u, i);
   }
   load_tokens(now);
   uint32_t buffer = 0;
-  f32x4 acc[MT][2];
+  f32x4 acc[MT][NT];
   for (uint64_t task = first_task; task < end_task;) {
     if (now.segment == 0) {
 #pragma unroll
-      for (uint32_t m = 0; m < MT; ++m) acc[m][0] = acc[m][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      for (uint32_t m = 0; m < MT; ++m)
+#pragma unroll
+        for (uint32_t i = 0; i < NT; ++i) acc[m][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
     Task next = now;
     const bool last_segment = ++next.segment == p.segments;
@@ -381,33 +382,34 @@ __global__ __launch_bounds__(kWaves *kWave) void k_mlp(Args p) {
     const bool more = !last_segment || task + 1 < end_task;
     if (more) settle(next);
     From f = from_of(more ? next : now);
-    if (!more) f.row[0] = f.row[1] = p.w;  // nothing is left to load: a line that all of the wave reads
+    if (!more) {  // nothing is left to load: a line that all of the wave reads
+#pragma unroll
+      for (uint32_t i = 0; i < NT; ++i) f.row[i] = p.w;
+    }
 #pragma unroll
     for (uint32_t u = 0; u < U; ++u) {
-      bf16x8 w[2][4];
-      typename F::Scale s[2];
+      const bool used = u < p.share && block_of(now.segment, u) < p.kblocks;
 #pragma unroll
-      for (uint32_t i = 0; i < 2; ++i) {
-        F::widen(raw[u][i], scale[u][i], q, w[i]);
-        s[i] = scale[u][i];
-      }
-      load(f, next, u);
-      if (u >= p.share || block_of(now.segment, u) >= p.kblocks) continue;
-#pragma unroll
-      for (uint32_t i = 0; i < 2; ++i)
+      for (uint32_t i = 0; i < NT; ++i) {
+        bf16x8 w[4];
+        const typename F::Scale s = scale[u][i];
+        F::widen(raw[u][i], s, q, w);
+        load(f, next, u, i);
+        if (!used) continue;
 #pragma unroll
         for (uint32_t m = 0; m < MT; ++m)
 #pragma unroll
-          for (uint32_t l = 0; l < kPlanes; ++l) acc[m][i] = F::add(acc[m][i], tok[u][m][l], w[i], s[i]);
+          for (uint32_t l = 0; l < kPlanes; ++l) acc[m][i] = F::add(acc[m][i], tok[u][m][l], w, s);
+      }
     }
     if (last_segment) {
 #pragma unroll
       for (uint32_t m = 0; m < MT; ++m)
 #pragma unroll
-        for (uint32_t i = 0; i < 2; ++i) red[buffer][wave][i][m][lane] = acc[m][i];
+        for (uint32_t i = 0; i < NT; ++i) red[buffer][wave][i][m][lane] = acc[m][i];
       lds_barrier();  // (the next task's sums go to the other buffer, so one is enough)
       for (uint32_t it = wave; it < 4 * kGroups; it += kWaves) {
-        const uint32_t group = it / 4, e = it % 4, m = GATED ? group : group / 2, i = GATED ? 0 : group % 2;
+        const uint32_t group = it / 4, e = it % 4, m = group / kWide, i = group % kWide;
         auto sum = [&](uint32_t i) {
           float v = red[buffer][0][i][m][lane][e];
 #pragma unroll
@@ -417,12 +419,12 @@ __global__ __launch_bounds__(kWaves *kWave) void k_mlp(Args p) {
         const float v = sum(i);
         const uint32_t place = 16 * m + 4 * q + e;
         if (OUT) {
-          const uint32_t c = now.strip * 32 + 16 * i + i16;  // (y's rows go on to the end of the strip)
+          const uint32_t c = (now.strip * kWide + i) * 16 + i16;  // (y's rows go on to the end of the strip)
           if (place < count) y_of(p)[static_cast<uint64_t>(of_pass[wave][place]) * p.y_pitch + c] = v;
         } else {
-          const uint32_t unit = now.strip * (GATED ? 16 : 32) + 16 * i + i16;
+          const uint32_t unit = (now.strip * kWide + i) * 16 + i16;
           // units past the last one, up to the block's end, are zeros
-          const float h = unit < p.hidden ? (GATED ? silu(v) * sum(1) : silu(v)) : 0.0f;
+          const float h = unit < p.hidden ? (GATED ? silu(v) * sum(kWide + i) : silu(v)) : 0.0f;
           if (place < count && unit < p.h_pitch) {
             const uint64_t at = static_cast<uint64_t>(of_pass[wave][place]) * p.h_pitch + unit;
             const uint32_t hi = bf16_pair(h, 0.0f) & 0xFFFF;
@@ -460,38 +462,38 @@ __global__ __launch_bounds__(kCombineThreads) void k_mlp_combine(Args p, uint32_
 }
 
 uint32_t h_pitch(uint64_t hidden) { return static_cast<uint32_t>((hidden + kBlock - 1) / kBlock * kBlock); }
-uint32_t y_pitch(uint64_t cols) { return static_cast<uint32_t>((cols + kTaskRows - 1) / kTaskRows * kTaskRows); }
+uint32_t y_pitch(uint64_t cols) { return static_cast<uint32_t>((cols + kMostRows - 1) / kMostRows * kMostRows); }
 
 constexpr uint32_t kWorkgroups = 256;  // one a CU
 
-template <typename F, uint32_t U, uint32_t MT, bool OUT, bool WHOLE = true>
+template <typename F, uint32_t U, uint32_t MT, uint32_t NT, bool OUT, bool WHOLE = true>
 hipError_t launch_product(Args a, bool gated, hipStream_t s) {
   a.kblocks = (a.k + kBlock - 1) / kBlock;
   a.segments = (a.kblocks + kWaves * U - 1) / (kWaves * U);
   a.share = (a.kblocks + kWaves * a.segments - 1) / (kWaves * a.segments);
   // rows of h up to the end of its last block, so that what the second kernel reads is written
-  a.strips = OUT ? a.y_pitch / 32 : a.h_pitch / (gated ? 16 : 32);
+  a.strips = (OUT ? a.y_pitch : a.h_pitch) / (gated ? 8 * NT : 16 * NT);
   const uint64_t passes = min(a.experts, a.slots) + a.slots / (16 * MT);
   const dim3 grid(static_cast<uint32_t>(min(static_cast<uint64_t>(kWorkgroups), passes * a.strips)));
-  if (gated) hipLaunchKernelGGL((k_mlp<F, U, MT, OUT, !OUT, WHOLE>), grid, dim3(kWaves * kWave), 0, s, a);
-  else hipLaunchKernelGGL((k_mlp<F, U, MT, OUT, false, WHOLE>), grid, dim3(kWaves * kWave), 0, s, a);
+  if (gated) hipLaunchKernelGGL((k_mlp<F, U, MT, NT, OUT, !OUT, WHOLE>), grid, dim3(kWaves * kWave), 0, s, a);
+  else hipLaunchKernelGGL((k_mlp<F, U, MT, NT, OUT, false, WHOLE>), grid, dim3(kWaves * kWave), 0, s, a);
   return hipGetLastError();
 }
 
-// What the registers hold of a wave's share of k: blocks U times tokens 16 MT (times two numbers for h).
+// What the registers hold of a wave's share of k: blocks U times tokens 16 MT (times two numbers for h), and weights
+// U times rows 16 NT. Two passes over an expert's weights beat one with MT 2 while few experts have over 16 tokens.
 hipError_t launch_hidden(const Args &a, bool fp8, bool gated, hipStream_t s) {
   const uint32_t share = (a.k + kBlock * kWaves - 1) / (kBlock * kWaves);
-  const bool few = a.slots <= 16;
-  if (a.k % 8 != 0) return fp8 ? launch_product<F8, 2, 1, false, false>(a, gated, s) : launch_product<Mx, 2, 1, false, false>(a, gated, s);
-  if (fp8) return share <= 2 ? launch_product<F8, 2, 1, false>(a, gated, s) : launch_product<F8, 5, 1, false>(a, gated, s);
-  if (few) return share <= 2 ? launch_product<Mx, 2, 1, false>(a, gated, s) : launch_product<Mx, 4, 1, false>(a, gated, s);
-  return share <= 2 ? launch_product<Mx, 2, 2, false>(a, gated, s) : launch_product<Mx, 4, 2, false>(a, gated, s);
+  if (a.k % 8 != 0) return fp8 ? launch_product<F8, 2, 1, 4, false, false>(a, gated, s) : launch_product<Mx, 2, 1, 4, false, false>(a, gated, s);
+  if (fp8) return share <= 2 ? launch_product<F8, 2, 1, 4, false>(a, gated, s) : launch_product<F8, 5, 1, 2, false>(a, gated, s);
+  if (a.slots <= 12 * a.experts) return share <= 2 ? launch_product<Mx, 2, 1, 4, false>(a, gated, s) : launch_product<Mx, 4, 1, 4, false>(a, gated, s);
+  return share <= 2 ? launch_product<Mx, 2, 2, 4, false>(a, gated, s) : launch_product<Mx, 4, 2, 2, false>(a, gated, s);
 }
 hipError_t launch_out(const Args &a, bool fp8, hipStream_t s) {
   const uint32_t share = (a.k + kBlock * kWaves - 1) / (kBlock * kWaves);
-  if (fp8) return launch_product<F8, 2, 1, true>(a, false, s);
-  if (share > 2) return launch_product<Mx, 4, 1, true>(a, false, s);
-  return a.slots <= 16 ? launch_product<Mx, 2, 1, true>(a, false, s) : launch_product<Mx, 2, 2, true>(a, false, s);
+  if (fp8) return launch_product<F8, 2, 1, 4, true>(a, false, s);
+  if (share > 2) return launch_product<Mx, 4, 1, 2, true>(a, false, s);
+  return a.slots <= 12 * a.experts ? launch_product<Mx, 2, 1, 4, true>(a, false, s) : launch_product<Mx, 2, 2, 2, true>(a, false, s);
 }
 
 }  // namespace

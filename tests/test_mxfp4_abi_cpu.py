@@ -103,7 +103,7 @@ def test_expert_mlp_workspace():
     size = nv.load().nvfp4_expert_mlp_workspace_bytes
     assert size(0, 2, 64, 64) % 16 == 0 and size(0, 2, 64, 64) > 0
     assert size(64, 8, 4096, 2048) - size(0, 8, 4096, 2048) == 512 * 4 * (2048 + 4096)
-    assert size(3, 1, 33, 129) - size(0, 1, 33, 129) == 3 * 4 * (256 + 64)
+    assert size(3, 1, 65, 129) - size(0, 1, 65, 129) == 3 * 4 * (256 + 128)
     assert size(513, 2, 64, 64) == size(1, 1, 64, 0) == size(1, 1, 0, 64) == size(-1, 1, 64, 64) == size(1, 0, 64, 64) == 0
 
 
