@@ -22,12 +22,13 @@
 // Both products run in the same form: one workgroup a CU, which takes a run of
 // tasks, each 16 NT rows of one expert's weights (gated: two rows for each of 8 NT
 // units) for up to 16 MT of its tokens, the blocks along k dealt out to eight waves,
-// whose sums meet in LDS: in the middle of the next task, since at a task's own end
+// whose sums meet in LDS: late in the next task, since at a task's own end
 // the waves waited for each other (64 tokens, 61 experts of 2 x 2048 x 4096: 141 -> 137 us
-// for the first product, 80 -> 76 for the second; 4.0 and 3.6 TB/s). The tokens' rows stay
-// in registers from task to task (where k fits them), and each register of weights
-// is asked for again, for the next task, as soon as it is widened, so that a CU has
-// 64 KB on their way all the time.
+// for the first product, 80 -> 76 for the second). The tokens' rows stay in registers
+// from task to task (where k fits them), and each register of weights is asked
+// for again, for the next task, as soon as it is widened. A row's blocks are
+// asked for one after the other, since a line of 128 bytes holds two: 143 -> 123
+// us and 80 -> 70.
 #include "codec.h"
 #include "launch.h"
 #include "matmul.h"
@@ -356,7 +357,7 @@ __global__ __launch_bounds__(kWaves *kWave) void k_mlp(Args p) {
     }
   };
 
-  // A finished task's sums wait in LDS until the middle of the next one, when every wave's have long been there: the
+  // A finished task's sums wait in LDS until late in the next one, when every wave's have long been there: the
   // waves do not wait for each other, and the next weights are on their way meanwhile.
   uint32_t buffer = 0, waiting = 0;  // strip + 1 of the task that waits
   auto finish = [&] {
@@ -398,9 +399,9 @@ __global__ __launch_bounds__(kWaves *kWave) void k_mlp(Args p) {
   {
     const From f = from_of(now);
 #pragma unroll
-    for (uint32_t u = 0; u < U; ++u)
+    for (uint32_t i = 0; i < NT; ++i)
 #pragma unroll
-      for (uint32_t i = 0; i < NT; ++i) load(f, now, u, i);
+      for (uint32_t u = 0; u < U; ++u) load(f, now, u, i);
   }
   load_tokens(now);
   f32x4 acc[MT][NT];
@@ -425,14 +426,16 @@ __global__ __launch_bounds__(kWaves *kWave) void k_mlp(Args p) {
       for (uint32_t i = 0; i < NT; ++i) f.row[i] = p.w;
     }
 #pragma unroll
-    for (uint32_t u = 0; u < U; ++u) {
-      if (u == U / 2) finish();
-      const bool used = u < p.share && block_of(now.segment, u) < p.kblocks;
+    for (uint32_t i = 0; i < NT; ++i) {
+      if (i == NT - 1) finish();
 #pragma unroll
-      for (uint32_t i = 0; i < NT; ++i) {
+      for (uint32_t u = 0; u < U; ++u) {
+        const bool used = u < p.share && block_of(now.segment, u) < p.kblocks;
         bf16x8 w[4];
         const typename F::Scale s = scale[u][i];
         F::widen(raw[u][i], s, q, w);
+        // (widened by now: else the old registers would live past the loads, and be copied, all loads waited for, each task)
+        asm volatile("" : "+v"(w[0]), "+v"(w[1]), "+v"(w[2]), "+v"(w[3])::"memory");
         load(f, next, u, i);
         if (!used) continue;
 #pragma unroll
