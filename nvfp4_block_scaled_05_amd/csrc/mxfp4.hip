@@ -7,8 +7,9 @@
 //   X = 2^(s - 127); code = E2M1(v / X), nearest even, at most 6; 0 where s is 255
 //
 // which is 2^(floor(log2 m) - 2), clamped at 2^-127: |v / X| < 8, and what is
-// above 6 becomes 6. v / X is v times a power of two and exact, unless it
-// is below 2^-126, where the code is 0 anyway.
+// above 6 becomes 6. The gfx950 conversions to E2M1 divide by X and round
+// once; BF16 goes in as it is, two values a word, with no multiplication or
+// widening of its own (gathered rows both ways 111 -> 97 us).
 //
 // One workgroup per 128x128 tile, in registers: thread t holds the 8x8 patch
 // at rows 8 (t / 16), columns 8 (t % 16). Four neighbouring lanes hold a row's
@@ -18,7 +19,7 @@
 // Columns and rows past the end count as zeros; each orientation's rows are
 // padded to a multiple of 128 with zero codes, which every tile writes whole.
 // Bound by HBM: 2 (or 4) bytes read and half a byte a side written for each value.
-// 32 x 2048x4096 BF16 in 2D both ways takes 178 us, 4.6 TB/s, where a copy of 1 GiB on
+// 32 x 2048x4096 BF16 in 2D both ways takes 163 us, 5.0 TB/s, where a copy of 1 GiB on
 // the same card moves 5.1; reading it back to BF16 132 us, 5.2 TB/s.
 #include "codec.h"
 #include "launch.h"
@@ -32,9 +33,12 @@ constexpr uint32_t kTile = kFp8Block;
 constexpr uint32_t kPerWord = kTile / 8;  // words of a tile's row of codes
 
 // Inputs that the Infinity Cache (256 MB) is likely to hold, and gathered rows, which are read several times, are kept
-// there: the outputs are stored past the caches. 8192x5120 BF16 both ways 31.1 -> 27.9 us, 36736 gathered rows of
-// 5120 columns both ways 127 -> 111; but 8192x8192 51.9 -> 55.1 and 32 x 2048x4096 177 -> 186, which are not.
+// there: the outputs are stored past the caches. 8192x5120 BF16 both ways 29.8 -> 26.6 us, 36736 gathered rows of
+// 5120 columns both ways 118 -> 97; but 8192x8192 47 -> 53 and 32 x 2048x4096 163 -> 169, which are not.
 constexpr uint64_t kStreamBelow = uint64_t{1} << 27;
+// For the others a workgroup asks for LDS that it does not use, so that six are on a CU, not eight, whose reads and stores
+// are too far apart: 32 x 2048x4096 both ways 180 us with eight, 171 with seven, 163 with six, 173 with five, 172 with four.
+constexpr uint32_t kIdleLds = 7680;
 
 struct Args {
   const void *x;
@@ -52,17 +56,43 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits) {
   const uint32_t e = amax_bits >> 23;
   return e == 255 ? 255 : e > 2 ? e - 2 : 0;
 }
-// 1 / X; 0 for the NaN scale, whose infinities and NaN encode() then drops.
-__device__ __forceinline__ float inverse(uint32_t s) { return __uint_as_float((254 - s) << 23); }
-
-// Eight values of a block with scale byte s.
-__device__ __forceinline__ uint32_t encode(const float *v, uint32_t s) {
-  const float e = inverse(s);
-  float t[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) t[i] = v[i] * e;
-  const uint32_t w = e2m1_rne_x8(t);
+// The codes of eight values, in a row's or a column's order, of a block with scale byte s. The conversions divide by a
+// power of two, whose exponent field they take from the scale as the byte is (0: 2^-127), exactly, and round once.
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t encode(const uint32_t *pairs, uint32_t s) {
+  const float x = __uint_as_float(s << 23);
+  uint32_t w = pairs[0];  // (all of it is written)
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2, pairs[0]), x, 0);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2, pairs[1]), x, 1);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2, pairs[2]), x, 2);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2, pairs[3]), x, 3);
   return s == 255 ? 0 : w;
+}
+__device__ __forceinline__ uint32_t encode(const float *v, uint32_t s) {
+  const float x = __uint_as_float(s << 23);
+  uint32_t w = __float_as_uint(v[0]);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[0], v[1], x, 0);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[2], v[3], x, 1);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[4], v[5], x, 2);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6], v[7], x, 3);
+  return s == 255 ? 0 : w;
+}
+__device__ __forceinline__ uint32_t encode_row(const Patch<kBF16> &v, int p, uint32_t s) {
+  const uint32_t pairs[4] = {v.w[p][0], v.w[p][1], v.w[p][2], v.w[p][3]};
+  return encode(pairs, s);
+}
+__device__ __forceinline__ uint32_t encode_col(const Patch<kBF16> &v, int q, uint32_t s) {
+  uint32_t pairs[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) pairs[i] = __builtin_amdgcn_perm(v.w[2 * i + 1][q / 2], v.w[2 * i][q / 2], q % 2 ? 0x07060302 : 0x05040100);
+  return encode(pairs, s);
+}
+__device__ __forceinline__ uint32_t encode_row(const Patch<kFP32> &v, int p, uint32_t s) { return encode(v.v[p], s); }
+__device__ __forceinline__ uint32_t encode_col(const Patch<kFP32> &v, int q, uint32_t s) {
+  float f[8];
+#pragma unroll
+  for (int p = 0; p < 8; ++p) f[p] = v.v[p][q];
+  return encode(f, s);
 }
 
 // Where the word of row i and column group g of a tile is: eight rows take 16
@@ -130,10 +160,7 @@ __global__ __launch_bounds__(kThreads) void k_mxfp4_quantize(Args a) {
       w |= dpp_mov<0x141>(w);
       w |= dpp_mov<0x140>(w);
       mine = cg == p ? w : mine;
-      float f[8];
-#pragma unroll
-      for (int q = 0; q < 8; ++q) f[q] = v.get(p, q);
-      straight[place(8 * rg + p, cg)] = encode(f, s);
+      straight[place(8 * rg + p, cg)] = encode_row(v, p, s);
     }
     const uint32_t r = r0 + 8 * rg + cg;
     if (cg < 8 && r < a.rows) a.row_scales[(static_cast<uint64_t>(batch) * a.col_tiles + ct) * a.rows + r] = mine;
@@ -142,10 +169,7 @@ __global__ __launch_bounds__(kThreads) void k_mxfp4_quantize(Args a) {
 #pragma unroll
     for (uint32_t q = 0; q < 8; ++q) {
       const uint32_t s = BLOCK_2D ? both : scale_byte(col_max[q]);
-      float f[8];
-#pragma unroll
-      for (int p = 0; p < 8; ++p) f[p] = v.get(p, q);
-      turned[place(8 * cg + q, rg)] = encode(f, s);
+      turned[place(8 * cg + q, rg)] = encode_col(v, q, s);
       if (lane < 16) col_bytes[8 * cg + q][wave] = static_cast<uint8_t>(s);
     }
   }
@@ -238,7 +262,7 @@ hipError_t launch(const Args &a, hipStream_t s) {
   if (a.tiles == 0) return hipSuccess;
   const uint64_t in = static_cast<uint64_t>(a.tiles) * kTile * kTile * (DT == kBF16 ? 2 : 4);
   if (a.row_slots != nullptr || in < kStreamBelow) hipLaunchKernelGGL((k_mxfp4_quantize<DT, BLOCK_2D, true>), long_grid(a.tiles), dim3(kThreads), 0, s, a);
-  else hipLaunchKernelGGL((k_mxfp4_quantize<DT, BLOCK_2D, false>), long_grid(a.tiles), dim3(kThreads), 0, s, a);
+  else hipLaunchKernelGGL((k_mxfp4_quantize<DT, BLOCK_2D, false>), long_grid(a.tiles), dim3(kThreads), kIdleLds, s, a);
   return hipGetLastError();
 }
 

@@ -513,8 +513,8 @@ hipError_t launch_tile(const Mxfp4Matmul &p, hipStream_t s) {
 //   Few rows, dense, and columns for at most a workgroup of 64x64 tiles a CU, against the tiles below:
 //     1 x 8192 x 5120     5.1 / 8.2      32 x 8192 x 5120  7.2 / 8.3     32 x 2048 x 2048  4.3 / 5.6
 //     but 64 x 8192 x 5120  10.2 / 8.5;  16 x 28672 x 8192  31 / 23
-//   Groups of up to 64 rows on average, by the buffer's rows: 64 rows high, against 128x128 tiles and
-//   the few-row kernel by groups, which that rule had until then:
+//   Groups of up to 64 rows on average, by the buffer's rows: 64 rows high, against 128x128 tiles
+//   and a kernel of few rows by groups:
 //     64 groups, 1472 rows x 4096 x 2048  51 / 63 / 78      32 groups, 992 rows  27 / 28 / 37
 //     64 groups, 4096 rows x 4096 x 2048  63 / 71 / 132
 //   Up to one tile a CU the waves share the blocks along k, in the smallest tiles for which that holds:
