@@ -21,7 +21,8 @@
 //
 // Both products run in the same form: one workgroup a CU, which takes a run of
 // tasks, each 16 NT rows of one expert's weights (gated: two rows for each of 8 NT
-// units) for up to 16 MT of its tokens, the blocks along k dealt out to eight waves,
+// units) for up to 16 MT of its tokens, the blocks along k dealt out to eight waves
+// (or, where rows are short, to fewer, beside others with rows of their own),
 // whose sums meet in LDS: late in the next task, since at a task's own end
 // the waves waited for each other (64 tokens, 61 experts of 2 x 2048 x 4096: 141 -> 137 us
 // for the first product, 80 -> 76 for the second). The tokens' rows stay in registers
@@ -115,7 +116,7 @@ struct F8 {
 constexpr uint32_t kTable = 4, kList = kTable + 3 * kMaxGroups, kHidden = (kList + kMlpMaxSlots) * 4;
 static_assert(kHidden % 16 == 0, "h is aligned");
 
-constexpr uint32_t kWaves = 8, kMostRows = 64;  // of a task
+constexpr uint32_t kWaves = 8, kMostRows = 64;  // of a wave's task
 
 struct Args {
   const uint16_t *x;
@@ -130,6 +131,7 @@ struct Args {
   uint32_t cols, hidden, h_pitch, y_pitch;
   uint32_t n, k, kblocks;
   uint32_t strips;           // tasks that an expert's rows make
+  uint32_t along, across;    // waves that share a row's blocks, and groups of them, each with rows of its own
   uint32_t segments, share;  // parts of k that the registers hold at a time; blocks of one that a wave takes
 };
 
@@ -195,8 +197,9 @@ __device__ __forceinline__ void slots_of(const uint16_t *ids, uint32_t slots, ui
 }
 
 // U blocks along k a wave and segment at most, 16 MT tokens a pass, 16 NT rows a task. OUT: y from h, else h from x.
-// WHOLE: k is a multiple of 8.
-template <typename F, uint32_t U, uint32_t MT, uint32_t NT, bool OUT, bool GATED, bool WHOLE>
+// WHOLE: k is a multiple of 8. SHORT: fewer than all waves share a row (else what depends on it is constant, which a token's layer
+// takes 35.6 us with, not 36.6).
+template <typename F, uint32_t U, uint32_t MT, uint32_t NT, bool OUT, bool GATED, bool WHOLE, bool SHORT>
 __global__ __launch_bounds__(kWaves *kWave) void k_mlp(Args p) {
   constexpr uint32_t kPlanes = OUT ? 2 : 1, kTokens = 16 * MT;
   constexpr uint32_t kWide = GATED ? NT / 2 : NT, kGroups = MT * kWide;  // results of 16 x 16 of a task
@@ -207,6 +210,8 @@ __global__ __launch_bounds__(kWaves *kWave) void k_mlp(Args p) {
   __shared__ uint32_t of_pass[kWaves][kTokens];  // each wave's own copy
   const uint32_t lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const uint32_t i16 = lane % 16, q = lane / 16;
+  const uint32_t along = SHORT ? p.along : kWaves, across = SHORT ? p.across : 1;
+  const uint32_t wk = wave & (along - 1), wr = wave >> __builtin_ctz(along);
 
   if (OUT) {
     for (uint32_t i = threadIdx.x; i < kMaxGroups; i += kWaves * kWave) {
@@ -292,14 +297,14 @@ __global__ __launch_bounds__(kWaves *kWave) void k_mlp(Args p) {
     const uint8_t *scales;
     uint32_t at[NT];  // rows of the matrix; those past the end repeat the last one, and their results are not used
   };
-  auto block_of = [&](uint32_t segment, uint32_t u) { return (segment * kWaves + wave) * p.share + u; };
+  auto block_of = [&](uint32_t segment, uint32_t u) { return (segment * along + wk) * p.share + u; };
   auto from_of = [&](const Task &t) {
     From f;
     const uint8_t *matrix = p.w + static_cast<uint64_t>(t.expert) * p.n * pitch;
     f.scales = static_cast<const uint8_t *>(p.scales) + t.expert * scale_bytes;
 #pragma unroll
     for (uint32_t i = 0; i < NT; ++i) {
-      f.at[i] = min((t.strip * kWide + i % kWide) * 16 + i16, (OUT ? p.n : p.hidden) - 1) + i / kWide * p.hidden;
+      f.at[i] = min(((t.strip * across + wr) * kWide + i % kWide) * 16 + i16, (OUT ? p.n : p.hidden) - 1) + i / kWide * p.hidden;
       f.row[i] = matrix + f.at[i] * pitch;
     }
     return f;
@@ -365,25 +370,27 @@ __global__ __launch_bounds__(kWaves *kWave) void k_mlp(Args p) {
     lds_barrier();
     const uint32_t strip = waiting - 1;
     waiting = 0;
-    for (uint32_t it = wave; it < 4 * kGroups; it += kWaves) {
-      const uint32_t group = it / 4, e = it % 4, m = group / kWide, i = group % kWide;
+    for (uint32_t it = wave; it < 4 * kGroups * across; it += kWaves) {
+      const uint32_t rows = it / (4 * kGroups), group = it / 4 % kGroups, e = it % 4, m = group / kWide, i = group % kWide;
       auto sum = [&](uint32_t i) {
-        float v = red[buffer ^ 1][0][i][m][lane][e];
+        const f32x4(*from)[NT][MT][kWave] = &red[buffer ^ 1][rows * along];
+        float v = from[0][i][m][lane][e];
 #pragma unroll
-        for (uint32_t k = 1; k < kWaves; ++k) v += red[buffer ^ 1][k][i][m][lane][e];
+        for (uint32_t k = 1; k < kWaves; ++k) {
+          if (k == along) break;
+          v += from[k][i][m][lane][e];
+        }
         return v;
       };
       const float v = sum(i);
-      const uint32_t place = 16 * m + 4 * q + e;
+      const uint32_t place = 16 * m + 4 * q + e, c = ((strip * across + rows) * kWide + i) * 16 + i16;
       if (OUT) {
-        const uint32_t c = (strip * kWide + i) * 16 + i16;  // (y's rows go on to the end of the strip)
-        if (place < count) y_of(p)[static_cast<uint64_t>(of_pass[wave][place]) * p.y_pitch + c] = v;
+        if (place < count && c < p.y_pitch) y_of(p)[static_cast<uint64_t>(of_pass[wave][place]) * p.y_pitch + c] = v;
       } else {
-        const uint32_t unit = (strip * kWide + i) * 16 + i16;
         // units past the last one, up to the block's end, are zeros
-        const float h = unit < p.hidden ? (GATED ? silu(v) * sum(kWide + i) : silu(v)) : 0.0f;
-        if (place < count && unit < p.h_pitch) {
-          const uint64_t at = static_cast<uint64_t>(of_pass[wave][place]) * p.h_pitch + unit;
+        const float h = c < p.hidden ? (GATED ? silu(v) * sum(kWide + i) : silu(v)) : 0.0f;
+        if (place < count && c < p.h_pitch) {
+          const uint64_t at = static_cast<uint64_t>(of_pass[wave][place]) * p.h_pitch + c;
           const uint32_t hi = bf16_pair(h, 0.0f) & 0xFFFF;
           // (where the rounding is no number, or infinite, so that the sum shall be, the rest is nothing)
           const float rest = h - __uint_as_float(hi << 16);
@@ -486,14 +493,29 @@ constexpr uint32_t kWorkgroups = 256;  // one a CU
 template <typename F, uint32_t U, uint32_t MT, uint32_t NT, bool OUT, bool WHOLE = true>
 hipError_t launch_product(Args a, bool gated, hipStream_t s) {
   a.kblocks = (a.k + kBlock - 1) / kBlock;
-  a.segments = (a.kblocks + kWaves * U - 1) / (kWaves * U);
-  a.share = (a.kblocks + kWaves * a.segments - 1) / (kWaves * a.segments);
   // rows of h up to the end of its last block, so that what the second kernel reads is written
-  a.strips = (OUT ? a.y_pitch : a.h_pitch) / (gated ? 8 * NT : 16 * NT);
+  const uint32_t wide = gated ? 8 * NT : 16 * NT, results = OUT ? a.y_pitch : a.h_pitch;
+  // Rows shorter than what eight waves hold are shared by fewer, which take more rows at a time, while there is a task for
+  // every CU. A layer of 64 tokens, 64 experts of 2 x 512 x 4096 in MXFP4 78 -> 62 us, 2 x 512 x 1024 43 -> 35; of 128 tokens
+  // and 2 x 2944 x 128 in FP8 117 -> 49.
+  constexpr bool kMayBeShort = U == 2;  // (the other kernels are for rows that are not)
+  for (a.along = kMayBeShort ? 1 : kWaves;; a.along *= 2) {
+    a.across = kWaves / a.along;
+    a.strips = (results + wide * a.across - 1) / (wide * a.across);
+    if (a.along == kWaves || (a.kblocks <= a.along * U && static_cast<uint64_t>(min(a.experts, a.slots)) * a.strips >= kWorkgroups)) break;
+  }
+  a.segments = (a.kblocks + a.along * U - 1) / (a.along * U);
+  a.share = (a.kblocks + a.along * a.segments - 1) / (a.along * a.segments);
   const uint64_t passes = min(a.experts, a.slots) + a.slots / (16 * MT);
   const dim3 grid(static_cast<uint32_t>(min(static_cast<uint64_t>(kWorkgroups), passes * a.strips)));
-  if (gated) hipLaunchKernelGGL((k_mlp<F, U, MT, NT, OUT, !OUT, WHOLE>), grid, dim3(kWaves * kWave), 0, s, a);
-  else hipLaunchKernelGGL((k_mlp<F, U, MT, NT, OUT, false, WHOLE>), grid, dim3(kWaves * kWave), 0, s, a);
+  if (kMayBeShort && a.along < kWaves) {
+    if (gated) hipLaunchKernelGGL((k_mlp<F, U, MT, NT, OUT, !OUT, WHOLE, kMayBeShort>), grid, dim3(kWaves * kWave), 0, s, a);
+    else hipLaunchKernelGGL((k_mlp<F, U, MT, NT, OUT, false, WHOLE, kMayBeShort>), grid, dim3(kWaves * kWave), 0, s, a);
+  } else if (gated) {
+    hipLaunchKernelGGL((k_mlp<F, U, MT, NT, OUT, !OUT, WHOLE, false>), grid, dim3(kWaves * kWave), 0, s, a);
+  } else {
+    hipLaunchKernelGGL((k_mlp<F, U, MT, NT, OUT, false, WHOLE, false>), grid, dim3(kWaves * kWave), 0, s, a);
+  }
   return hipGetLastError();
 }
 

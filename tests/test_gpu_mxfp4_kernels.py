@@ -75,7 +75,12 @@ LAYERS = [(3, 2, 4, 8200, 136), (2, 2, 4, 5300, 96), (3, 2, 4, 136, 4200), (1, 1
           (33, 2, 2, 120, 4168), (30, 2, 2, 4100, 136), (512, 2, 3, 1000, 520), (1024, 1, 1, 72, 40), (300, 3, 20, 2049, 130), (13, 1, 1, 8192, 8192), (12, 1, 1, 256, 256)]
 
 
-@pytest.mark.parametrize("tokens,topk,experts,cols,hidden", LAYERS)
+# rows of few blocks, which fewer waves share, with strips that end past the results
+SHORT = [(100, 3, 64, 256, 1300), (100, 3, 64, 2100, 200), (500, 2, 64, 250, 1400), (500, 2, 64, 2100, 200), (64, 8, 64, 1000, 300), (40, 4, 128, 130, 2000),
+         (90, 2, 64, 520, 700), (512, 2, 64, 400, 600)]
+
+
+@pytest.mark.parametrize("tokens,topk,experts,cols,hidden", LAYERS + SHORT)
 @pytest.mark.parametrize("kind", ["mxfp4", "fp8"])
 @pytest.mark.parametrize("gated", [True, False])
 def test_layers(tokens, topk, experts, cols, hidden, kind, gated):
