@@ -520,19 +520,26 @@ hipError_t launch_product(Args a, bool gated, hipStream_t s) {
 }
 
 // What the registers hold of a wave's share of k: blocks U times tokens 16 MT (times two numbers for h), and weights
-// U times rows 16 NT. Two passes over an expert's weights beat one with MT 2 while few experts have over 16 tokens.
+// U times rows 16 NT. Two passes over an expert's weights beat one with MT 2 while few experts have over 16 tokens: a layer
+// in FP8 of 2 x 768 x 2048, 128 tokens for all of 8 experts 80 / 60 us; 2 x 1024 x 2048, 64 experts, 16 slots each 123 / 111,
+// 14 each 112 / 114.
 hipError_t launch_hidden(const Args &a, bool fp8, bool gated, hipStream_t s) {
+  const bool two = a.slots > 12 * a.experts;
   const uint32_t share = (a.k + kBlock * kWaves - 1) / (kBlock * kWaves);
   if (a.k % 8 != 0) return fp8 ? launch_product<F8, 2, 1, 4, false, false>(a, gated, s) : launch_product<Mx, 2, 1, 4, false, false>(a, gated, s);
-  if (fp8) return share <= 2 ? launch_product<F8, 2, 1, 4, false>(a, gated, s) : launch_product<F8, 5, 1, 2, false>(a, gated, s);
-  if (a.slots <= 12 * a.experts) return share <= 2 ? launch_product<Mx, 2, 1, 4, false>(a, gated, s) : launch_product<Mx, 4, 1, 4, false>(a, gated, s);
-  return share <= 2 ? launch_product<Mx, 2, 2, 4, false>(a, gated, s) : launch_product<Mx, 4, 2, 2, false>(a, gated, s);
+  if (fp8) {
+    if (share > 2) return launch_product<F8, 5, 1, 2, false>(a, gated, s);
+    return two ? launch_product<F8, 2, 2, 4, false>(a, gated, s) : launch_product<F8, 2, 1, 4, false>(a, gated, s);
+  }
+  if (two) return share <= 2 ? launch_product<Mx, 2, 2, 4, false>(a, gated, s) : launch_product<Mx, 4, 2, 2, false>(a, gated, s);
+  return share <= 2 ? launch_product<Mx, 2, 1, 4, false>(a, gated, s) : launch_product<Mx, 4, 1, 4, false>(a, gated, s);
 }
 hipError_t launch_out(const Args &a, bool fp8, hipStream_t s) {
+  const bool two = a.slots > 12 * a.experts;
   const uint32_t share = (a.k + kBlock * kWaves - 1) / (kBlock * kWaves);
-  if (fp8) return launch_product<F8, 2, 1, 4, true>(a, false, s);
+  if (fp8) return two && share <= 2 ? launch_product<F8, 2, 2, 2, true>(a, false, s) : launch_product<F8, 2, 1, 4, true>(a, false, s);
   if (share > 2) return launch_product<Mx, 4, 1, 2, true>(a, false, s);
-  return a.slots <= 12 * a.experts ? launch_product<Mx, 2, 1, 4, true>(a, false, s) : launch_product<Mx, 2, 2, 2, true>(a, false, s);
+  return two ? launch_product<Mx, 2, 2, 2, true>(a, false, s) : launch_product<Mx, 2, 1, 4, true>(a, false, s);
 }
 
 }  // namespace
