@@ -146,12 +146,23 @@ __device__ __forceinline__ uint32_t id_of(const Args &p, uint32_t slot) {
   return id < 0 || id >= p.experts ? p.experts : static_cast<uint32_t>(id);
 }
 
-// Eight values of a row of x from `at` on, zeros from `cols` on.
-__device__ __forceinline__ bf16x8 tokens8(const uint16_t *row, uint32_t at, uint32_t cols) {
+// A row's first eight values, of which there are fewer.
+__device__ __forceinline__ bf16x8 tokens_of_few(const uint16_t *row, uint32_t cols) {
   uint32_t e[8];
 #pragma unroll
-  for (uint32_t i = 0; i < 8; ++i) e[i] = at + i < cols ? row[at + i] : 0u;
+  for (uint32_t i = 0; i < 8; ++i) e[i] = i < cols ? row[i] : 0u;
   return __builtin_bit_cast(bf16x8, u32x4{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16});
+}
+
+// Eight values without the first `drop`, and zeros behind them.
+__device__ __forceinline__ bf16x8 without(bf16x8 v, uint32_t drop) {
+  typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
+  u64x2 w = __builtin_bit_cast(u64x2, v);
+  const uint32_t bits = 16 * (drop % 4);
+  const uint64_t carry = bits == 0 ? 0 : w.y << (64 - bits);
+  const u64x2 near{w.x >> bits | carry, w.y >> bits};
+  w = drop < 4 ? near : u64x2{near.y, 0};
+  return __builtin_bit_cast(bf16x8, drop < 8 ? w : u64x2{0, 0});
 }
 
 __device__ __forceinline__ float silu(float v) { return v / (1.0f + __expf(-v)); }
@@ -347,7 +358,17 @@ __global__ __launch_bounds__(kWaves *kWave) void k_mlp(Args p) {
               tok[u][m][l][e] = __builtin_bit_cast(bf16x8, OUT || at < p.cols ? w : u32x4{0, 0, 0, 0});
             }
       }
+    } else if (p.cols < 8) {
+#pragma unroll
+      for (uint32_t u = 0; u < U; ++u)
+#pragma unroll
+        for (uint32_t m = 0; m < MT; ++m)
+#pragma unroll
+          for (uint32_t e = 0; e < 4; ++e)
+            tok[u][m][0][e] = e == 0 && q == 0 ? tokens_of_few(row[m], p.cols) : __builtin_bit_cast(bf16x8, u32x4{0, 0, 0, 0});
     } else {
+      // Rows start anywhere, which the loads may; a piece that ends past the row is the row's last eight, some of them dropped.
+      // (Value by value, 64 tokens and 2 x 512 x 4100 in MXFP4 took 160 us, not 92.)
 #pragma unroll
       for (uint32_t u = 0; u < U; ++u) {
         const uint32_t kb = min(block_of(t.segment, min(u, p.share - 1)), p.kblocks - 1);
@@ -355,9 +376,11 @@ __global__ __launch_bounds__(kWaves *kWave) void k_mlp(Args p) {
         for (uint32_t m = 0; m < MT; ++m)
 #pragma unroll
           for (uint32_t e = 0; e < 4; ++e) {
-            tok[u][m][0][e] = tokens8(row[m], kb * kBlock + F::at(q, e), p.cols);
-            __builtin_amdgcn_sched_barrier(0);  // (else all of them are on their way at once, in eight registers each)
+            const uint32_t at = kb * kBlock + F::at(q, e), from = min(at, p.cols - 8);
+            const u32x4 w = *reinterpret_cast<const u32x4_any *>(row[m] + from);
+            tok[u][m][0][e] = without(__builtin_bit_cast(bf16x8, w), at - from);
           }
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
   };
@@ -526,7 +549,10 @@ hipError_t launch_product(Args a, bool gated, hipStream_t s) {
 hipError_t launch_hidden(const Args &a, bool fp8, bool gated, hipStream_t s) {
   const bool two = a.slots > 12 * a.experts;
   const uint32_t share = (a.k + kBlock * kWaves - 1) / (kBlock * kWaves);
-  if (a.k % 8 != 0) return fp8 ? launch_product<F8, 2, 1, 4, false, false>(a, gated, s) : launch_product<Mx, 2, 1, 4, false, false>(a, gated, s);
+  if (a.k % 8 != 0) {  // (with U 4 and 5 no faster: 2 x 512 x 4100 92 / 91 us, one token's 29.4 / 30.9)
+    if (fp8) return two ? launch_product<F8, 2, 2, 4, false, false>(a, gated, s) : launch_product<F8, 2, 1, 4, false, false>(a, gated, s);
+    return two ? launch_product<Mx, 2, 2, 4, false, false>(a, gated, s) : launch_product<Mx, 2, 1, 4, false, false>(a, gated, s);
+  }
   if (fp8) {
     if (share > 2) return launch_product<F8, 5, 1, 2, false>(a, gated, s);
     return two ? launch_product<F8, 2, 2, 4, false>(a, gated, s) : launch_product<F8, 2, 1, 4, false>(a, gated, s);
