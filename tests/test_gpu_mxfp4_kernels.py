@@ -77,7 +77,7 @@ LAYERS = [(3, 2, 4, 8200, 136), (2, 2, 4, 5300, 96), (3, 2, 4, 136, 4200), (1, 1
 
 # rows of few blocks, which fewer waves share, with strips that end past the results
 SHORT = [(100, 3, 64, 256, 1300), (100, 3, 64, 2100, 200), (500, 2, 64, 250, 1400), (500, 2, 64, 2100, 200), (64, 8, 64, 1000, 300), (40, 4, 128, 130, 2000),
-         (90, 2, 64, 520, 700), (512, 2, 64, 400, 600)]
+         (90, 2, 64, 520, 700), (512, 2, 64, 400, 600), (5, 2, 8, 9, 40), (3, 2, 4, 7, 24), (20, 1, 1, 15, 9), (6, 2, 3, 127, 33)]
 
 
 @pytest.mark.parametrize("tokens,topk,experts,cols,hidden", LAYERS + SHORT)
