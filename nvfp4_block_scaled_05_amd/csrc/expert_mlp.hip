@@ -90,21 +90,30 @@ struct F8 {
   }
   static __host__ __device__ uint64_t scale_bytes(uint32_t n, uint32_t kblocks) { return static_cast<uint64_t>((n + kBlock - 1) / kBlock) * kblocks * 4; }
   static __device__ __forceinline__ uint32_t at(uint32_t q, uint32_t p) { return p / 2 * 64 + 16 * q + p % 2 * 8; }
-  static __device__ __forceinline__ void widen(const Raw &r, Scale, uint32_t, bf16x8 *f) {
+  // A scale's power of two goes into the widened codes, its mantissa to the block's sum: codes are up to 448, so sums of codes
+  // times x leave binary32's range where the weights' do not. (Powers from 2^-117 to 2^119 keep every code's product with them
+  // a normal BF16 number, 2^-126 to 1.75 * 2^127; what a scale has beyond stays with the mantissa.)
+  static __device__ __forceinline__ float power(Scale s) {
+    constexpr uint32_t least = (127u - 117) << 23, most = (127u + 119) << 23;
+    return __uint_as_float(min(max(__float_as_uint(s) & 0x7F800000u, least), most));
+  }
+  static __device__ __forceinline__ void widen(const Raw &r, Scale s, uint32_t, bf16x8 *f) {
+    const float scale = power(s);
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
       const uint32_t x = r.w[p / 2][p % 2 * 2], y = r.w[p / 2][p % 2 * 2 + 1];
-      const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, 1.0f, false), b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, 1.0f, true);
-      const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(y, 1.0f, false), d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(y, 1.0f, true);
+      const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, scale, false), b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, scale, true);
+      const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(y, scale, false), d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(y, scale, true);
       f[p] = bf16x8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
     }
   }
   static __device__ __forceinline__ f32x4 add(f32x4 acc, const bf16x8 *t, const bf16x8 *w, Scale s) {
+    const float rest = s * __uint_as_float((254u << 23) - __float_as_uint(power(s)));  // over the power of two, exactly
     f32x4 c{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int p = 0; p < 4; ++p) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(t[p], w[p], c, 0, 0, 0);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(c[e], s, acc[e]);
+    for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(c[e], rest, acc[e]);
     return acc;
   }
 };
