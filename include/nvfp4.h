@@ -599,8 +599,10 @@ uint64_t nvfp4_expert_mlp_workspace_bytes(int64_t tokens, int64_t topk, int64_t 
  * and act(g, u) = silu(g) u of its first and second half; 0: hidden rows and act =
  * silu. w2[e] has cols rows of hidden values. w1 and w2 are batches of `experts`
  * matrices, MXFP4 or FP8 in 128x128 blocks. x and out are BF16 [tokens][cols],
- * 16-byte aligned, any cols and hidden from 1 to 2^23 - 1. Sums are held in FP32,
- * act's results in 16 bits of mantissa. Only the experts that ids names are read.
+ * 16-byte aligned, any cols and hidden from 1 to 2^23 - 1. Scales may be any (under
+ * 255, MXFP4's NaN, a row's sum is NaN); rows of MXFP4 with scales above 252 take
+ * far longer. Sums are held in FP32, so one that leaves its range is an infinity or
+ * NaN; act's results in 16 bits of mantissa. Only the experts that ids names are read.
  * tokens * topk at most NVFP4_EXPERT_MLP_MAX_SLOTS, experts in 1 ..
  * NVFP4_MAX_GROUPS. workspace: 16-byte aligned, at least
  * nvfp4_expert_mlp_workspace_bytes(); its contents do not matter, and calls that

@@ -7,8 +7,8 @@
 // act(g, u) = silu(g) u for the two halves of w1's rows, or silu(g); weights in
 // MXFP4 or block-scaled FP8 (128x128 blocks), x and out BF16. Bound by reading
 // the weights of the experts in use, once each; so the codes are widened to BF16
-// in registers (exact: E2M1 values times a power of two, and E4M3 values, are
-// BF16 values) and multiplied by v_mfma_f32_16x16x32_bf16, which sums to binary32,
+// in registers (exact: E2M1 and E4M3 values times a power of two are BF16 values,
+// but for the powers at the ends of the range, see Mx and F8) and multiplied by v_mfma_f32_16x16x32_bf16, which sums to binary32,
 // and no activation is quantized. h goes from the first kernel to the second as
 // two BF16 numbers, its rounding and the rest's, 16 bits of mantissa together: with
 // one, out is 1.4 times as far off (2.4e-3 in the 2-norm, of which out's own
@@ -58,15 +58,47 @@ struct Mx {
   static __host__ __device__ uint64_t scale_bytes(uint32_t n, uint32_t kblocks) { return static_cast<uint64_t>(n) * kblocks * 4; }
   // value of the token's row that piece p (0 .. 3) of 8 begins at
   static __device__ __forceinline__ uint32_t at(uint32_t q, uint32_t p) { return 32 * q + 8 * p; }
-  static __device__ __forceinline__ void widen(const Raw &r, Scale s, uint32_t q, bf16x8 *f) {
-    // the conversion takes its scale's exponent field as the byte: 0 is 2^-127, 255 NaN
-    const float x = __uint_as_float(s >> (8 * q) << 23);
+  static __device__ __forceinline__ void widen(const Raw &r, Scale s, uint32_t q, bf16x8 *f) { widen_by(r, min(byte_of(s, q), kMostByte), f); }
+  // the conversion takes its scale's exponent field as the byte: 0 is 2^-127, 255 NaN
+  static __device__ __forceinline__ void widen_by(const Raw &r, uint32_t byte, bf16x8 *f) {
+    const float x = __uint_as_float(byte << 23);
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
       const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(r.w[p], x, 0), b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(r.w[p], x, 1);
       const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(r.w[p], x, 2), d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(r.w[p], x, 3);
       f[p] = bf16x8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
     }
+  }
+  static __device__ __forceinline__ uint32_t byte_of(Scale s, uint32_t q) { return s >> (8 * q) & 255; }
+  // Under scales 253 and 254 the larger codes are past BF16's range, where an infinity would be wrong, and no number times a zero of
+  // x or h: all are widened under 252 at most, and rows with a larger byte (255, which is NaN, among them) are summed again, at the
+  // kernel's end. (Within the loop that cost calls that never come there up to 2% of their time, 128 tokens for 8 experts of
+  // 2 x 2048 x 4096 108.5 -> 111 us, beside each fragment's products 114: scalar registers run out.)
+  static constexpr bool kSumsAgain = true;
+  static constexpr uint32_t kMostByte = 252;
+  static __device__ __forceinline__ void watch(uint32_t &most, Scale s, uint32_t q) { most = max(most, byte_of(s, q)); }
+  static __device__ __forceinline__ bool row_lacks(const void *scales, uint32_t n, uint32_t kblocks, uint32_t r) {
+    uint32_t most = 0;
+    for (uint32_t piece = 0; piece < kblocks * 4; ++piece) most = max(most, byte_of(scale(scales, n, piece / 4, r), piece % 4));
+    return most > kMostByte;
+  }
+  // Row r of a matrix times `token(k)`, summed in binary64.
+  template <typename T>
+  static __device__ __forceinline__ float sum_again(const uint8_t *matrix, const void *scales, uint32_t n, uint32_t kblocks, uint32_t r, T token) {
+    const uint8_t *row = matrix + static_cast<uint64_t>(r) * kblocks * kRowBytes;
+    double sum = 0.0;
+    for (uint32_t piece = 0; piece < kblocks * 4; ++piece) {  // of 32 values
+      typedef float f2 __attribute__((ext_vector_type(2)));
+      double of_piece = 0.0;
+      for (uint32_t at = 0; at < 32; at += 2) {
+        const f2 w = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(row[static_cast<uint64_t>(piece) * 16 + at / 2], 1.0f, 0);
+        of_piece += static_cast<double>(w.x) * token(piece * 32 + at);
+        of_piece += static_cast<double>(w.y) * token(piece * 32 + at + 1);
+      }
+      const uint32_t b = byte_of(scale(scales, n, piece / 4, r), piece % 4);
+      sum += b < 255 ? ldexp(of_piece, static_cast<int>(b) - 127) : __builtin_nan("");
+    }
+    return static_cast<float>(sum);
   }
   static __device__ __forceinline__ f32x4 add(f32x4 acc, const bf16x8 *t, const bf16x8 *w, Scale) {
 #pragma unroll
@@ -90,6 +122,7 @@ struct F8 {
   }
   static __host__ __device__ uint64_t scale_bytes(uint32_t n, uint32_t kblocks) { return static_cast<uint64_t>((n + kBlock - 1) / kBlock) * kblocks * 4; }
   static __device__ __forceinline__ uint32_t at(uint32_t q, uint32_t p) { return p / 2 * 64 + 16 * q + p % 2 * 8; }
+  static constexpr bool kSumsAgain = false;
   // A scale's power of two goes into the widened codes, its mantissa to the block's sum: codes are up to 448, so sums of codes
   // times x leave binary32's range where the weights' do not. (Powers from 2^-117 to 2^119 keep every code's product with them
   // a normal BF16 number, 2^-126 to 1.75 * 2^127; what a scale has beyond stays with the mantissa.)
@@ -228,6 +261,7 @@ __global__ __launch_bounds__(kWaves *kWave) void k_mlp(Args p) {
   __shared__ Lists lists;
   __shared__ uint16_t ids[OUT ? 1 : kMlpMaxSlots];
   __shared__ uint32_t of_pass[kWaves][kTokens];  // each wave's own copy
+  __shared__ uint32_t again;                     // rows may have to be summed again
   const uint32_t lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const uint32_t i16 = lane % 16, q = lane / 16;
   const uint32_t along = SHORT ? p.along : kWaves, across = SHORT ? p.across : 1;
@@ -294,6 +328,7 @@ __global__ __launch_bounds__(kWaves *kWave) void k_mlp(Args p) {
     }
   }
   if (wave == 0) count_passes(lists, kTokens);
+  if (F::kSumsAgain && threadIdx.x == 0) again = 0;
   lds_barrier();
 
   // this workgroup's tasks: pass after pass, strip after strip
@@ -336,7 +371,7 @@ __global__ __launch_bounds__(kWaves *kWave) void k_mlp(Args p) {
   };
   bf16x8 tok[U][MT][kPlanes][4];
   uint32_t count = 0;  // the pass's tokens
-  auto load_tokens = [&](const Task &t) {
+  auto list_tokens = [&](const Task &t) {
     const uint32_t first = (t.pass - __builtin_amdgcn_readfirstlane(lists.passes[t.rank])) * kTokens;
     count = min(kTokens, __builtin_amdgcn_readfirstlane(lists.count[t.rank]) - first);
     if (OUT) {
@@ -345,6 +380,9 @@ __global__ __launch_bounds__(kWaves *kWave) void k_mlp(Args p) {
       slots_of(ids, p.slots, t.expert, first, kTokens, of_pass[wave]);
     }
     __builtin_amdgcn_wave_barrier();
+  };
+  auto load_tokens = [&](const Task &t) {
+    list_tokens(t);
     const uint16_t *row[MT];
 #pragma unroll
     for (uint32_t m = 0; m < MT; ++m) {
@@ -394,6 +432,25 @@ __global__ __launch_bounds__(kWaves *kWave) void k_mlp(Args p) {
     }
   };
 
+  // Column c of a slot's row, from its row's sum and, gated, the second half's (asked for when the first is done with: both at a time
+  // are more than the registers hold).
+  auto put = [&](uint32_t slot, uint32_t c, float v, auto up) {
+    if (OUT) {
+      if (c < p.y_pitch) y_of(p)[static_cast<uint64_t>(slot) * p.y_pitch + c] = v;
+      return;
+    }
+    // units past the last one, up to the block's end, are zeros
+    const float h = c < p.hidden ? (GATED ? silu(v) * up() : silu(v)) : 0.0f;
+    if (c < p.h_pitch) {
+      const uint64_t at = static_cast<uint64_t>(slot) * p.h_pitch + c;
+      const uint32_t hi = bf16_pair(h, 0.0f) & 0xFFFF;
+      // (where the rounding is no number, or infinite, so that the sum shall be, the rest is nothing)
+      const float rest = h - __uint_as_float(hi << 16);
+      h_of(p, 0)[at] = static_cast<uint16_t>(hi);
+      h_of(p, 1)[at] = static_cast<uint16_t>(bf16_pair(fabsf(rest) <= fabsf(h) ? rest : 0.0f, 0.0f));
+    }
+  };
+
   // A finished task's sums wait in LDS until late in the next one, when every wave's have long been there: the
   // waves do not wait for each other, and the next weights are on their way meanwhile.
   uint32_t buffer = 0, waiting = 0;  // strip + 1 of the task that waits
@@ -414,22 +471,9 @@ __global__ __launch_bounds__(kWaves *kWave) void k_mlp(Args p) {
         }
         return v;
       };
-      const float v = sum(i);
       const uint32_t place = 16 * m + 4 * q + e, c = ((strip * across + rows) * kWide + i) * 16 + i16;
-      if (OUT) {
-        if (place < count && c < p.y_pitch) y_of(p)[static_cast<uint64_t>(of_pass[wave][place]) * p.y_pitch + c] = v;
-      } else {
-        // units past the last one, up to the block's end, are zeros
-        const float h = c < p.hidden ? (GATED ? silu(v) * sum(kWide + i) : silu(v)) : 0.0f;
-        if (place < count && c < p.h_pitch) {
-          const uint64_t at = static_cast<uint64_t>(of_pass[wave][place]) * p.h_pitch + c;
-          const uint32_t hi = bf16_pair(h, 0.0f) & 0xFFFF;
-          // (where the rounding is no number, or infinite, so that the sum shall be, the rest is nothing)
-          const float rest = h - __uint_as_float(hi << 16);
-          h_of(p, 0)[at] = static_cast<uint16_t>(hi);
-          h_of(p, 1)[at] = static_cast<uint16_t>(bf16_pair(fabsf(rest) <= fabsf(h) ? rest : 0.0f, 0.0f));
-        }
-      }
+      const float v = sum(i);
+      if (place < count) put(of_pass[wave][place], c, v, [&] { return sum(kWide + i); });
     }
   };
 
@@ -444,6 +488,7 @@ __global__ __launch_bounds__(kWaves *kWave) void k_mlp(Args p) {
   }
   load_tokens(now);
   f32x4 acc[MT][NT];
+  uint32_t most = 0;  // scale byte that this lane has seen
   for (uint64_t task = first_task; task < end_task;) {
     if (now.segment == 0) {
 #pragma unroll
@@ -473,6 +518,7 @@ __global__ __launch_bounds__(kWaves *kWave) void k_mlp(Args p) {
         bf16x8 w[4];
         const typename F::Scale s = scale[u][i];
         F::widen(raw[u][i], s, q, w);
+        if constexpr (F::kSumsAgain) F::watch(most, s, q);
         // (widened by now: else the old registers would live past the loads, and be copied, all loads waited for, each task)
         asm volatile("" : "+v"(w[0]), "+v"(w[1]), "+v"(w[2]), "+v"(w[3])::"memory");
         load(f, next, u, i);
@@ -496,6 +542,31 @@ __global__ __launch_bounds__(kWaves *kWave) void k_mlp(Args p) {
     if (!more || (other_tokens && next.pass != now.pass)) finish();  // of this pass's tokens
     if (other_tokens) load_tokens(next);
     now = next;
+  }
+
+  if constexpr (F::kSumsAgain) {
+    if (__any(most > F::kMostByte)) again = 1;
+    __syncthreads();  // (and all results are stored)
+    if (__builtin_amdgcn_readfirstlane(again) == 0) return;
+    const uint32_t wide = across * kWide * 16;  // columns of a task
+    Task t{0, 0, 0, 0, 0};
+    for (uint64_t task = first_task; task < end_task; ++task) {
+      t.pass = static_cast<uint32_t>(task / p.strips), t.strip = static_cast<uint32_t>(task % p.strips);
+      settle(t);
+      list_tokens(t);
+      const uint8_t *matrix = p.w + static_cast<uint64_t>(t.expert) * p.n * pitch, *scales = static_cast<const uint8_t *>(p.scales) + t.expert * scale_bytes;
+      for (uint32_t it = threadIdx.x; it < wide * count; it += kWaves * kWave) {
+        const uint32_t slot = of_pass[wave][it / wide], c = t.strip * wide + it % wide;
+        if (c >= (OUT ? p.n : p.hidden)) continue;
+        auto token = [&](uint32_t k) {
+          if (OUT) return bf16_lo(h_of(p, 0)[static_cast<uint64_t>(slot) * p.h_pitch + k]) + bf16_lo(h_of(p, 1)[static_cast<uint64_t>(slot) * p.h_pitch + k]);
+          return k < p.cols ? bf16_lo(p.x[static_cast<uint64_t>(slot / p.topk) * p.cols + k]) : 0.0f;
+        };
+        if (!F::row_lacks(scales, p.n, p.kblocks, c) && !(GATED && F::row_lacks(scales, p.n, p.kblocks, c + p.hidden))) continue;
+        const float v = F::sum_again(matrix, scales, p.n, p.kblocks, c, token);
+        put(slot, c, v, [&] { return F::sum_again(matrix, scales, p.n, p.kblocks, c + p.hidden, token); });
+      }
+    }
   }
 }
 

@@ -5,6 +5,7 @@ from __future__ import annotations
 import pytest
 import torch
 
+import mxfp4_helpers as M
 import nvfp4_block_scaled_05_amd as nv
 from gpu_helpers import DEV
 from test_gpu_expert_mlp import check, gen, layer
@@ -75,3 +76,97 @@ def test_fp8_every_code_under_every_power_of_two(hidden):
         want = (torch.exp2(powers)[:, None] * value * 2.0 ** power).float().bfloat16()
         assert torch.equal(out[:, :127], want), power
         assert not bool(out[:, 127].any())
+
+
+# ---- MXFP4 ----------------------------------------------------------------------
+
+CODES = torch.tensor(list(M.E2M1) + list(-M.E2M1), dtype=torch.float64)
+SCALES = (0, 1, 2, 127, 251, 252, 253, 254)
+
+
+def table(rows_at, pitch, n):
+    """Rows of every code under every scale of SCALES, at value 32 q of a row for q = row % 4 (of block `rows_at`), and again at the
+    value after it: an Mxfp4Tensor of n rows, and each row's value and q."""
+    kb = pitch // 128
+    data = torch.zeros((1, n, pitch // 2), dtype=torch.uint8)
+    scales = torch.full((1, kb, n, 4), 127, dtype=torch.uint8)
+    value, place = torch.zeros(n, dtype=torch.float64), torch.zeros(n, dtype=torch.long)
+    for r in range(n):
+        code, s, q = r // 4 % 16, SCALES[r // 64 % len(SCALES)], r % 4
+        at = 128 * rows_at + 32 * q
+        data[0, r, at // 2] = code | code << 4
+        scales[0, rows_at, r, q] = s
+        value[r], place[r] = CODES[code] * 2.0 ** (s - 127), at
+    return data, scales, value.to(DEV), place.to(DEV)
+
+
+ROWS = 4 * 16 * len(SCALES)
+
+
+@pytest.mark.parametrize("tokens", [1, 40])
+@pytest.mark.parametrize("cols", [512, 2304, 4224])
+@pytest.mark.parametrize("gated", [True, False])
+def test_every_code_under_the_scales_of_both_ends_in_the_first_product(tokens, cols, gated):
+    data, scales, value, place = table(1, cols, ROWS)
+    if gated:  # the second half's rows are 1 in the first column
+        up, ups = torch.zeros_like(data), torch.full_like(scales, 127)
+        up[0, :, 0] = 2
+        data, scales = torch.cat([data, up], 1), torch.cat([scales, ups], 2)
+    w1 = nv.Mxfp4Tensor(data.to(DEV), scales.to(DEV), (1 + gated) * ROWS, cols)
+    w2 = nv.mxfp4_quantize(torch.eye(cols, ROWS, device=DEV)[None])[0]
+    ids, weights = torch.zeros((tokens, 1), dtype=torch.int32, device=DEV), torch.ones((tokens, 1), device=DEV)
+    for power in (-100, -4):
+        x = torch.zeros((tokens, cols), dtype=torch.bfloat16, device=DEV)
+        x[:, 0], x[:, 128:256:32] = 1, 2.0 ** power  # (the value next to each is zero)
+        out = nv.expert_mlp(x, ids, weights, w1, w2, gated=gated)[:, :ROWS].double()
+        v = value * 2.0 ** power  # (at most 6 * 2^123)
+        want = v * torch.sigmoid(v)
+        # an exponential is off by a few 2^-24 for each unit of its argument, of which 100 count
+        miss = (out - want).abs()
+        assert bool((miss <= want.abs() * (2.0 ** -8 + 2.0 ** -14) + 2.0 ** -126).all()), power
+
+
+@pytest.mark.parametrize("tokens", [1, 40])
+@pytest.mark.parametrize("hidden", [256, 2304])
+def test_every_code_under_the_scales_of_both_ends_in_the_second_product(tokens, hidden):
+    data, scales, value, place = table(1, hidden, ROWS)
+    w1 = torch.zeros((1, hidden, ROWS), device=DEV)
+    w1[0, 128:256:32, 5] = 1
+    w1, w2 = nv.mxfp4_quantize(w1)[0], nv.Mxfp4Tensor(data.to(DEV), scales.to(DEV), ROWS, hidden)
+    ids, weights = torch.zeros((tokens, 1), dtype=torch.int32, device=DEV), torch.ones((tokens, 1), device=DEV)
+    for power, h in ((-40, -41), (40, 40)):  # silu halves what is small and leaves what is large
+        x = torch.zeros((tokens, ROWS), dtype=torch.bfloat16, device=DEV)
+        x[:, 5] = 2.0 ** power
+        out = nv.expert_mlp(x, ids, weights, w1, w2, gated=False)
+        want = (value * 2.0 ** h).float().bfloat16()
+        assert torch.equal(out, want.expand(tokens, -1)), power
+
+
+@pytest.mark.parametrize("tokens,topk,experts,cols,hidden", SIZES)
+@pytest.mark.parametrize("gated", [True, False])
+def test_mxfp4_weights_of_the_largest_scales(tokens, topk, experts, cols, hidden, gated):
+    x, ids, weights = given(tokens, topk, experts, cols, 5)
+    x[:, ::3] = 0
+    for first in (True, False):
+        w1, w2 = layer("mxfp4", experts, cols, hidden, gated, 6)
+        q = w1 if first else w2
+        q.scales = torch.randint(249, 255, q.scales.shape, device=DEV, generator=gen(7)).to(torch.uint8)
+        # x or h makes up for them: the products' sums, and h of a gated layer, stay inside
+        run((x * 2.0 ** (-110 if first else -50 if gated else -100)).bfloat16(), ids, weights, w1, w2, gated, first)
+
+
+@pytest.mark.parametrize("tokens", [1, 50])
+@pytest.mark.parametrize("cols", [200, 2300])
+def test_mxfp4_rows_under_nan(tokens, cols):
+    x, ids, weights = given(tokens, 1, 3, cols, 8)
+    w1, w2 = layer("mxfp4", 3, cols, 264, True, 9)
+    want = nv.expert_mlp(x.bfloat16(), ids, weights, w1, w2)
+    w2.scales[1, 1, 77, 3] = 255
+    out = nv.expert_mlp(x.bfloat16(), ids, weights, w1, w2)
+    nan = torch.zeros((tokens, cols), dtype=torch.bool, device=DEV)
+    nan[:, 77] = ids[:, 0] == 1
+    assert torch.equal(torch.isnan(out), nan) and torch.equal(out[~nan], want[~nan])
+    w1.scales[2, 0, 264 + 100, 0] = 255  # one unit, which every column takes
+    out = nv.expert_mlp(x.bfloat16(), ids, weights, w1, w2)
+    nan[ids[:, 0] == 2] = True
+    assert torch.equal(torch.isnan(out), nan) and torch.equal(out[~nan], want[~nan])
