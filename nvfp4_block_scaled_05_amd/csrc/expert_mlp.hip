@@ -443,11 +443,12 @@ __global__ __launch_bounds__(kWaves *kWave) void k_mlp(Args p) {
     const float h = c < p.hidden ? (GATED ? silu(v) * up() : silu(v)) : 0.0f;
     if (c < p.h_pitch) {
       const uint64_t at = static_cast<uint64_t>(slot) * p.h_pitch + c;
-      const uint32_t hi = bf16_pair(h, 0.0f) & 0xFFFF;
-      // (where the rounding is no number, or infinite, so that the sum shall be, the rest is nothing)
+      uint32_t hi = bf16_pair(h, 0.0f) & 0xFFFF;
+      if ((hi & 0x7FFF) == 0x7F80 && fabsf(h) < __builtin_inff()) --hi;  // (past BF16's largest number by less than a step: that number)
+      // (where h is no number, or infinite, so that the sum shall be, the rest is nothing)
       const float rest = h - __uint_as_float(hi << 16);
       h_of(p, 0)[at] = static_cast<uint16_t>(hi);
-      h_of(p, 1)[at] = static_cast<uint16_t>(bf16_pair(fabsf(rest) <= fabsf(h) ? rest : 0.0f, 0.0f));
+      h_of(p, 1)[at] = static_cast<uint16_t>(bf16_pair(rest == rest ? rest : 0.0f, 0.0f));
     }
   };
 

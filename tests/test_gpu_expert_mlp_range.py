@@ -170,3 +170,49 @@ def test_mxfp4_rows_under_nan(tokens, cols):
     out = nv.expert_mlp(x.bfloat16(), ids, weights, w1, w2)
     nan[ids[:, 0] == 2] = True
     assert torch.equal(torch.isnan(out), nan) and torch.equal(out[~nan], want[~nan])
+
+
+# ---- both -----------------------------------------------------------------------
+
+def one_layer(kind, gate, up, out):
+    """Weights for 128 columns and 32 units, of one expert: unit 0's gate (and its up row, if any) as {column: power of two}, and row c of
+    w2 the power of two out[c] for unit 0; row c of w2 that is not in out is zero."""
+    units = 32 if up is None else 64
+
+    def pack(rows, n, k):
+        if kind == "fp8":
+            kb = 1
+            data = torch.zeros((1, n, 128), dtype=torch.uint8, device=DEV)
+            powers = {p for at in rows.values() for p in at.values()}
+            assert len(powers) == 1  # one block's scale
+            for r, at in rows.items():
+                for c in at:
+                    data[0, r, c] = 0x38
+            return nv.Fp8Tensor(data.view(torch.float8_e4m3fn), torch.full((1, kb, 1), 2.0 ** powers.pop(), device=DEV), n, k, True)
+        data = torch.zeros((1, n, 64), dtype=torch.uint8, device=DEV)
+        scales = torch.full((1, 1, n, 4), 127, dtype=torch.uint8, device=DEV)
+        for r, at in rows.items():
+            for c, p in at.items():
+                data[0, r, c // 2] |= 2 << (4 * (c % 2))
+                scales[0, 0, r, c // 32] = 127 + p
+        return nv.Mxfp4Tensor(data, scales, n, k)
+
+    rows = {0: gate} if up is None else {0: gate, 32: up}
+    return pack(rows, units, 128), pack({c: {0: p} for c, p in out.items()}, 128, 32)
+
+
+@pytest.mark.parametrize("kind", ["mxfp4", "fp8"])
+def test_hidden_values_next_to_the_largest_number(kind):
+    # h between the largest BF16 number and the largest of binary32
+    most = 255 * 2.0 ** 120
+    w1, w2 = one_layer(kind, {0: 0, 1: 0}, None, {3: -20, 7: -20})
+    more = [0.0, 0.25, 0.5, 0.75, 0.96875]
+    x = torch.zeros((len(more), 128), dtype=torch.float64)
+    x[:, 0], x[:, 1] = most, torch.tensor(more) * 2.0 ** 120
+    ids, weights = torch.zeros((len(more), 1), dtype=torch.int32, device=DEV), torch.ones((len(more), 1), device=DEV)
+    out = nv.expert_mlp(x.bfloat16().to(DEV), ids, weights, w1, w2, gated=False)
+    want = (x.sum(1) * 2.0 ** -20).float().bfloat16().to(DEV)
+    keep = torch.zeros(128, dtype=torch.bool, device=DEV)
+    keep[3] = keep[7] = True
+    assert torch.equal(out[:, keep], want[:, None].expand(-1, 2))
+    assert not bool(out[:, ~keep].any())
