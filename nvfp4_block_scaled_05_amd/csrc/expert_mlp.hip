@@ -207,7 +207,13 @@ __device__ __forceinline__ bf16x8 without(bf16x8 v, uint32_t drop) {
   return __builtin_bit_cast(bf16x8, drop < 8 ? w : u64x2{0, 0});
 }
 
-__device__ __forceinline__ float silu(float v) { return v / (1.0f + __expf(-v)); }
+// Far below zero, where 1 + e^-v is e^-v and from -88.7 on past the largest number, v e^v, of e^(v / 2) twice: e^v has no exponent
+// left where the product has.
+__device__ __forceinline__ float silu(float v) {
+  const bool far = v < -80.0f;
+  const float e = __expf(far ? 0.5f * v : -v);
+  return far ? v * e * e : v / (1.0f + e);
+}
 
 // The experts in use, in order, and their slots.
 struct Lists {

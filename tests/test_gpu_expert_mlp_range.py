@@ -216,3 +216,18 @@ def test_hidden_values_next_to_the_largest_number(kind):
     keep[3] = keep[7] = True
     assert torch.equal(out[:, keep], want[:, None].expand(-1, 2))
     assert not bool(out[:, ~keep].any())
+
+
+@pytest.mark.parametrize("kind", ["mxfp4", "fp8"])
+def test_gates_far_below_zero(kind):
+    # silu(g) = g e^g is small there, not nothing: times u of 2^100 it is a number to be seen
+    gates = torch.tensor([-60.0, -79, -80, -80.5, -81, -87, -88, -88.5, -89, -90, -91, -95, -100, -103, -110, -200, -1000], dtype=torch.float64)
+    w1, w2 = one_layer(kind, {0: 0}, {1: 0}, {3: 0})
+    x = torch.zeros((gates.numel(), 128), dtype=torch.float64)
+    x[:, 0], x[:, 1] = gates, 2.0 ** 100
+    assert torch.equal(x.bfloat16().double(), x)
+    ids, weights = torch.zeros((gates.numel(), 1), dtype=torch.int32, device=DEV), torch.ones((gates.numel(), 1), device=DEV)
+    out = nv.expert_mlp(x.bfloat16().to(DEV), ids, weights, w1, w2)[:, 3].double().cpu()
+    want = gates * torch.exp(gates) * 2.0 ** 100  # (1 + e^g is 1)
+    # an exponential is off by a few 2^-24 for each unit of its argument; silu is a binary32 number, of steps of 2^-149 at least
+    assert bool(((out - want).abs() <= want.abs() * (2.0 ** -8 + 2.0 ** -14) + 2.0 ** (100 - 148)).all()), (out, want)
