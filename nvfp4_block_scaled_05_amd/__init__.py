@@ -876,7 +876,8 @@ def _want_mxfp4(q: Mxfp4Tensor, lead, n: int, k: int, device, what: str) -> None
 
 
 def mxfp4_dequantize(q: Mxfp4Tensor, *, out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
-    """The values of q, [n][k] or [B][n][k]; bfloat16 and float32 hold them exactly."""
+    """The values of q, [n][k] or [B][n][k]; bfloat16 and float32 hold them exactly, but for those of
+    scales 253 and 254 that are past their largest number: infinities."""
     dev = _on(q.data, "the tensor")
     code = _out_code(out_dtype)
     lead = tuple(q.data.shape[:-2])
@@ -954,7 +955,8 @@ def expert_mlp(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w1, w2
     = silu of the first half's products times the second half's, or (not gated) n =
     hidden and act = silu; w2 has n = cols and k = hidden. Both are Mxfp4Tensors
     or both Fp8Tensors in 128x128 blocks. Larger batches go through expert_sort
-    and the grouped products."""
+    and the grouped products, which are also the faster form from about 32 slots an
+    expert on (16 where rows are of 8192 values)."""
     dev = _on(x, "x")
     if x.dim() != 2 or x.dtype is not torch.bfloat16:
         raise ValueError(f"x must be bfloat16 [tokens][cols], got {x.dtype} {tuple(x.shape)}")

@@ -6,7 +6,8 @@
 //
 // act(g, u) = silu(g) u for the two halves of w1's rows, or silu(g); weights in
 // MXFP4 or block-scaled FP8 (128x128 blocks), x and out BF16. Bound by reading
-// the weights of the experts in use, once each; so the codes are widened to BF16
+// the weights of the experts in use, once each up to the 16 or 32 slots an expert
+// that a pass takes (from the L2s once more for each pass beyond); so the codes are widened to BF16
 // in registers (exact: E2M1 and E4M3 values times a power of two are BF16 values,
 // but for the powers at the ends of the range, see Mx and F8) and multiplied by v_mfma_f32_16x16x32_bf16, which sums to binary32,
 // and no activation is quantized. h goes from the first kernel to the second as
@@ -578,7 +579,8 @@ __global__ __launch_bounds__(kWaves *kWave) void k_mlp(Args p) {
 }
 
 // ---------------------------------------------------------------------------
-// out: four columns of a token to a thread, its slots in the order of the choices.
+// out: four columns of a token to a thread, its slots in the order of the choices, one after the other (a choice that is left out
+// is a branch, so each one's loads wait for those before).
 // ---------------------------------------------------------------------------
 constexpr uint32_t kCombineThreads = 256;
 __global__ __launch_bounds__(kCombineThreads) void k_mlp_combine(Args p, uint32_t per_row) {
@@ -630,9 +632,17 @@ hipError_t launch_product(Args a, bool gated, hipStream_t s) {
 }
 
 // What the registers hold of a wave's share of k: blocks U times tokens 16 MT (times two numbers for h), and weights
-// U times rows 16 NT. Two passes over an expert's weights beat one with MT 2 while few experts have over 16 tokens: a layer
-// in FP8 of 2 x 768 x 2048, 128 tokens for all of 8 experts 80 / 60 us; 2 x 1024 x 2048, 64 experts, 16 slots each 123 / 111,
-// 14 each 112 / 114.
+// U times rows 16 NT. Which MT, by the slots an expert on average over all experts (how they spread is not known here): one pass of 32
+// slots against two of 16, where most experts have more than 16. Times in us with MT 1 / 2, weights from HBM:
+//   slots an expert                      8          12         16         20         24         32         48         64         128
+//   32 experts of 2 x 1024 x 1024, FP8   39 / 43    51 / 44    54 / 46    59 / 48    64 / 63    71 / 70
+//     MXFP4                              33 / 36    42 / 38    45 / 39    49 / 42    51 / 56    58 / 64
+//   8 experts of 2 x 768 x 2048, FP8     28 / 28    31 / 30    39 / 31    38 / 32    38 / 35    46 / 47    55 / 44    63 / 57    77 / 57
+//     MXFP4                              23 / 25    26 / 26    32 / 28    32 / 29    31 / 31    39 / 42    45 / 39    50 / 51
+//   64 experts of 2 x 1024 x 2048, FP8              104 / 104  117 / 106;  MXFP4 76 / 77  87 / 80
+// so from 12 on; where some experts' slots pass 32 and take two passes of 32 (24 to 32 on average) MXFP4 loses up to a tenth by it.
+// Longer rows than the registers hold go in segments, and their tokens are loaded again for each: FP8 takes 16 tokens for those.
+// (MXFP4, 32 experts of 2 x 1024, 32 tokens for 4 each: 4096 columns 60 us, 4104 80, 8192 113; the weights at a copy's rate 42, 41, 84.)
 hipError_t launch_hidden(const Args &a, bool fp8, bool gated, hipStream_t s) {
   const bool two = a.slots > 12 * a.experts;
   const uint32_t share = (a.k + kBlock * kWaves - 1) / (kBlock * kWaves);

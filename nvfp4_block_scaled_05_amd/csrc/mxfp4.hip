@@ -9,7 +9,7 @@
 // which is 2^(floor(log2 m) - 2), clamped at 2^-127: |v / X| < 8, and what is
 // above 6 becomes 6. The gfx950 conversions to E2M1 divide by X and round
 // once; BF16 goes in as it is, two values a word, with no multiplication or
-// widening of its own (gathered rows both ways 111 -> 97 us).
+// widening of its own (36736 gathered rows both ways 111 -> 97 us, the input in the Infinity Cache).
 //
 // One workgroup per 128x128 tile, in registers: thread t holds the 8x8 patch
 // at rows 8 (t / 16), columns 8 (t % 16). Four neighbouring lanes hold a row's
@@ -20,7 +20,7 @@
 // padded to a multiple of 128 with zero codes, which every tile writes whole.
 // Bound by HBM: 2 (or 4) bytes read and half a byte a side written for each value.
 // 32 x 2048x4096 BF16 in 2D both ways takes 163 us, 5.0 TB/s, where a copy of 1 GiB on
-// the same card moves 5.1; reading it back to BF16 132 us, 5.2 TB/s.
+// the same card moves 5.1, FP32 285 us, 4.8; reading it back to BF16 132 us, 5.2 TB/s, to FP32 261, 4.7.
 #include "codec.h"
 #include "launch.h"
 #include "patch.h"
@@ -34,7 +34,8 @@ constexpr uint32_t kPerWord = kTile / 8;  // words of a tile's row of codes
 
 // Inputs that the Infinity Cache (256 MB) is likely to hold, and gathered rows, which are read several times, are kept
 // there: the outputs are stored past the caches. 8192x5120 BF16 both ways 29.8 -> 26.6 us, 36736 gathered rows of
-// 5120 columns both ways 118 -> 97; but 8192x8192 47 -> 53 and 32 x 2048x4096 163 -> 169, which are not.
+// 5120 columns both ways 118 -> 97 (call after call on one input; 116 to 123 where other calls come between); but
+// 8192x8192 47 -> 53 and 32 x 2048x4096 163 -> 169, which are not.
 constexpr uint64_t kStreamBelow = uint64_t{1} << 27;
 // For the others a workgroup asks for LDS that it does not use, so that six are on a CU, not eight, whose reads and stores
 // are too far apart: 32 x 2048x4096 both ways 180 us with eight, 171 with seven, 163 with six, 173 with five, 172 with four.
