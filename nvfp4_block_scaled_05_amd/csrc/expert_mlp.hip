@@ -7,13 +7,14 @@
 // act(g, u) = silu(g) u for the two halves of w1's rows, or silu(g); weights in
 // MXFP4 or block-scaled FP8 (128x128 blocks), x and out BF16. Bound by reading
 // the weights of the experts in use, once each up to the 16 or 32 slots an expert
-// that a pass takes (from the L2s once more for each pass beyond); so the codes are widened to BF16
-// in registers (exact: E2M1 and E4M3 values times a power of two are BF16 values,
-// but for the powers at the ends of the range, see Mx and F8) and multiplied by v_mfma_f32_16x16x32_bf16, which sums to binary32,
-// and no activation is quantized. h goes from the first kernel to the second as
-// two BF16 numbers, its rounding and the rest's, 16 bits of mantissa together: with
-// one, out is 1.4 times as far off (2.4e-3 in the 2-norm, of which out's own
-// rounding makes 1.7e-3). y is FP32.
+// that a pass takes (and from the L2s again for each further pass); so the codes
+// are widened to BF16 in registers (exact: E2M1 and E4M3 values times a power of
+// two are BF16 values, but for powers at the ends of the range, see Mx and F8) and
+// multiplied by v_mfma_f32_16x16x32_bf16, which sums to binary32, and no
+// activation is quantized. h goes from the first kernel to the second as two BF16
+// numbers, its rounding and the rest's, 16 bits of mantissa together: with one, out
+// is 1.4 times as far off (2.4e-3 in the 2-norm, of which out's own rounding makes
+// 1.7e-3). y is FP32.
 //
 // A wave's fragment of a block of 128 along k is 16 rows of weights: lane l has
 // 32 values of row l % 16, and of token l % 16's row the same 32, so which
